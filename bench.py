@@ -103,7 +103,7 @@ def decode_bytes(B, H, dk, dv, elem=2):
 KERNEL_SOURCES = {"prefill.hip": ["prefill.hip", "chunk_ops.h", "common.h"],
                   "prefill_pipe.hip": ["prefill_pipe.hip", "chunk_ops.h", "common.h"],
                   "prefill_cw.hip": ["prefill_cw.hip", "chunk_ops.h", "common.h"],
-                  "decode.hip": ["decode.hip", "common.h"]}
+                  "decode.hip": ["decode.hip", "decode_row.h", "common.h"]}
 
 
 def kernel_source_sha(name):

@@ -6,12 +6,17 @@ the forward and the backward both run in the library's kernels, this module
 only routes tensors.  Gradients flow to every tensor argument that requires
 them (grouped query/key heads included); the backward recomputes the forward
 states itself, so nothing but the inputs is saved.
+
+``linear_recurrence(x, g, beta=None, h0=None)`` does the same for the gated linear
+recurrence (``ops.linrec_fwd``, ``ops.linrec_bwd``); it saves the inputs and the
+fp32 state before every 16th token.
 """
 from __future__ import annotations
 
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -43,3 +48,26 @@ def delta_rule(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Differentiable chunkwise forward: (o, S_T) with gradients through delta_bwd."""
     return _DeltaRule.apply(variant, q, k, v, beta, g, wgate, S0)
+
+
+class _LinearRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, beta, h0):
+        o, h_T, states = ops.linrec_fwd(x, g, beta=beta, h0=h0, want_states=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x, g, beta, states)
+        return o, h_T
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO, dh_T):
+        x, g, beta, states = ctx.saved_tensors
+        gr = ops.linrec_bwd(x, g, states, dO.contiguous().to(x.dtype), beta=beta,
+                            dh_T=dh_T.contiguous().to(torch.float32), want_dh0=ctx.needs_input_grad[3])
+        return gr["dx"], gr["dg"], gr["dbeta"], gr["dh0"]
+
+
+def linear_recurrence(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
+                      h0: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable gated linear recurrence over [B, T, D]: (o, h_T), with gradients
+    for x, g, beta and h0 through linrec_bwd."""
+    return _LinearRecurrence.apply(x, g, beta, h0)

@@ -127,4 +127,68 @@ struct TttArgs {
 };
 hipError_t launch_ttt_pre(int variant, int dtype, const TttArgs& a, hipStream_t stream);
 
+// ---- gated linear recurrence ----
+struct LinrecArgs {
+    int B, T, D;
+    const void* x;         // [B,T,D]
+    const void* g;
+    const void* beta;      // [B,T,D] or nullptr (1)
+    const float* h0;       // [B,D] or nullptr (zero)
+    void* o;               // [B,T,D]
+    float* hT;             // [B,D] or nullptr; may equal h0
+    float* states;         // [B,ceil(T/16),D] or nullptr
+    void* ws = nullptr;    // linrec_workspace_bytes() bytes
+};
+struct LinrecBwdArgs {
+    int B, T, D;
+    const void* x;         // as the forward's
+    const void* g;
+    const void* beta;
+    const float* states;   // as the forward wrote it
+    const void* dO;        // [B,T,D]
+    const float* dhT;      // [B,D] or nullptr (zero)
+    void* dx;              // [B,T,D]
+    void* dg;
+    void* dbeta;           // nullptr exactly when beta is
+    float* dh0;            // [B,D] or nullptr
+    void* ws = nullptr;
+};
+struct LinrecStepArgs {
+    int B, D, n_pages;
+    const void* x;         // [B,D]
+    const void* g;
+    const void* beta;      // or nullptr
+    float* h;              // [n_pages,D], in place
+    const int* slots;      // [B] or nullptr (page b)
+    void* o;               // [B,D]
+};
+size_t linrec_fwd_workspace_bytes(int dtype, int B, int T, int D);
+size_t linrec_bwd_workspace_bytes(int dtype, int B, int T, int D);
+hipError_t launch_linrec_fwd(int dtype, const LinrecArgs& a, hipStream_t stream);
+hipError_t launch_linrec_bwd(int dtype, const LinrecBwdArgs& a, hipStream_t stream);
+hipError_t launch_linrec_step(int dtype, const LinrecStepArgs& a, hipStream_t stream);
+
+// ---- pool of state pages ----
+// The decode step on pages: a.S is the pool, row b's state page slots[b].
+hipError_t launch_decode_slots(int variant, int dtype, const DecodeArgs& a, int n_pages,
+                               const int* slots, hipStream_t stream);
+struct PagesCopyArgs {
+    int64_t page;          // floats per page
+    int n_pages, src_pages, n;
+    float* pool;           // [n_pages,page]
+    const int* dst;        // [n]
+    const float* src_pool; // [src_pages,page]; may equal pool
+    const int* src;        // [n]
+};
+struct PagesCompactArgs {
+    int64_t page;
+    int n_pages, n;
+    float* pool;           // [n_pages,page]
+    const int* slots;      // [n]
+    int* slots_out;        // [n]
+    int* n_live;           // [1]
+};
+hipError_t launch_pages_copy(const PagesCopyArgs& a, hipStream_t stream);
+hipError_t launch_pages_compact(const PagesCompactArgs& a, hipStream_t stream);
+
 }  // namespace dr

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libdeltarule.so`` (see include/deltarule.h).
+"""Thin ctypes binding of ``libdeltarule.so`` (see include/deltarule.h and
+include/deltarule_ext.h).
 
 Argument marshalling only: shapes and dtypes of torch device tensors are
 checked, outputs are allocated with torch when not supplied, and the call is
@@ -19,7 +20,12 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdeltarule.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "deltarule.h")
 
+EXT_HEADER = os.path.join(os.path.dirname(_PKG), "include", "deltarule_ext.h")
+
 ABI_VERSION = 5   # DR_ABI_VERSION of the header this binding follows
+EXT_VERSION = 1   # DR_EXT_VERSION, the same for deltarule_ext.h
+LINREC_BLOCK = 16     # DR_LINREC_BLOCK
+MAX_PAGES = 65536     # DR_MAX_PAGES
 VARIANTS = {"deltanet": 0, "gdn": 1, "kda": 2, "gdn2": 3, "fg2": 4}
 # forms whose beta is one value per key channel (the erase gate, or the step sizes)
 _CHANNEL_BETA = ("gdn2", "fg2")
@@ -33,6 +39,15 @@ class DrDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("dtype", ctypes.c_int32), ("H_k", ctypes.c_int32)]
+
+
+class LinrecDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class PagesDesc(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("n", ctypes.c_int32)]
 
 
 class DeltaRuleError(RuntimeError):
@@ -77,6 +92,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if lib.dr_abi_version() != ABI_VERSION:
         raise ImportError(f"{path} has ABI version {lib.dr_abi_version()}, the binding expects "
                           f"{ABI_VERSION}: rebuild it")
+    if not hasattr(lib, "dr_ext_version") or lib.dr_ext_version() != EXT_VERSION:
+        raise ImportError(f"{path} lacks the entry points of deltarule_ext.h, version {EXT_VERSION}: rebuild it")
+    i32, ld, pd = ctypes.c_int32, ctypes.POINTER(LinrecDesc), ctypes.POINTER(PagesDesc)
+    for name, args in (("delta_linrec_fwd_workspace_bytes", [ld, ctypes.POINTER(sz)]),
+                       ("delta_linrec_bwd_workspace_bytes", [ld, ctypes.POINTER(sz)]),
+                       ("delta_linrec_fwd", [ld] + [vp] * 8 + [sz, vp]),
+                       ("delta_linrec_bwd", [ld] + [vp] * 11 + [sz, vp]),
+                       ("delta_linrec_step", [ld] + [vp] * 4 + [i32] + [vp] * 3),
+                       ("delta_decode_slots", [ctypes.POINTER(DrDesc)] + [vp] * 7 + [i32] + [vp] * 3),
+                       ("delta_pages_copy", [pd, vp, vp, vp, i32, vp, vp]),
+                       ("delta_pages_compact", [pd] + [vp] * 5)):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -110,8 +138,9 @@ def _raise(status: int):
     raise DeltaRuleError(status, lib.dr_status_str(status).decode())
 
 
-def workspace_bytes(entry: str, desc: "DrDesc") -> int:
-    """Device workspace a call needs (``entry`` is "fwd", "bwd" or "ttt_pre")."""
+def workspace_bytes(entry: str, desc) -> int:
+    """Device workspace a call needs (``entry`` is "fwd", "bwd" or "ttt_pre" with a
+    DrDesc, "linrec_fwd" or "linrec_bwd" with a LinrecDesc)."""
     lib = load_library()
     n = ctypes.c_size_t(0)
     st = getattr(lib, f"delta_{entry}_workspace_bytes")(ctypes.byref(desc), ctypes.byref(n))
@@ -408,3 +437,276 @@ def ttt_pre(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bet
     if st != 0:
         _raise(st)
     return o, A_T, B_T
+
+
+# ---- gated linear recurrence and pool of state pages (include/deltarule_ext.h) ----
+
+def _gpu(name: str, t: torch.Tensor) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: expected a GPU tensor, got device {t.device}")
+    return t.device
+
+
+def _enqueue(dev: torch.device, stream, fn, *args, fresh=()):
+    """Call ``fn(*args, stream)`` with ``dev`` current, on ``stream`` or else the
+    device's current stream.  ``fresh``: tensors allocated for this call, marked as
+    used on ``stream`` when that is another one than the current."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _enqueue(dev, stream, fn, *args, fresh=fresh)
+    if stream is None:
+        handle = torch.cuda.current_stream().cuda_stream
+    else:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        handle = stream.cuda_stream
+        for t in fresh:
+            if t is not None:
+                t.record_stream(stream)
+    st = fn(*args, handle)
+    if st != 0:
+        _raise(st)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _linrec_workspace(entry: str, desc: LinrecDesc, dev, workspace: Optional[torch.Tensor]):
+    """(workspace tensor or None, its bytes, the tensor if allocated here)."""
+    need = workspace_bytes(entry, desc)
+    if need == 0:
+        return None, 0, None
+    if workspace is None:
+        fresh = torch.empty(need, dtype=torch.uint8, device=dev)
+        return fresh, need, fresh
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
+    return workspace, workspace.numel() * workspace.element_size(), None
+
+
+def _linrec_check(x, g, beta, dims: int):
+    dev = _gpu("x", x)
+    if x.dim() != dims:
+        raise ValueError(f"x: expected {dims} dimensions, got shape {tuple(x.shape)}")
+    if x.dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    _check("x", x, x.shape, x.dtype, dev)
+    _check("g", g, x.shape, x.dtype, dev)
+    if beta is not None:
+        _check("beta", beta, x.shape, x.dtype, dev)
+    return dev
+
+
+def linrec_fwd(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
+               h0: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+               h_T: Optional[torch.Tensor] = None, want_state: bool = True,
+               states: Optional[torch.Tensor] = None, want_states: bool = False, stream=None,
+               workspace: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + beta_t x_t over sequences.
+
+    x, g and beta (None = 1) [B, T, D]; h0 [B, D] fp32 (None = 0).  Returns
+    (o, h_T, states): every state in x's dtype, the last state in fp32 (None unless
+    wanted or given; ``h_T=h0`` updates in place) and the states that ``linrec_bwd``
+    needs (None unless wanted or given), [B, ceil(T / LINREC_BLOCK), D] fp32.
+    """
+    lib = load_library()
+    dev = _linrec_check(x, g, beta, 3)
+    B, T, D = x.shape
+    if h0 is not None:
+        _check("h0", h0, (B, D), torch.float32, dev)
+    fresh = []
+    if o is None:
+        o = torch.empty_like(x)
+        fresh.append(o)
+    else:
+        _check("o", o, (B, T, D), x.dtype, dev)
+    if h_T is None and want_state:
+        h_T = torch.empty((B, D), dtype=torch.float32, device=dev)
+        fresh.append(h_T)
+    elif h_T is not None:
+        _check("h_T", h_T, (B, D), torch.float32, dev)
+    sshape = (B, -(-T // LINREC_BLOCK), D)
+    if states is None and want_states:
+        states = torch.empty(sshape, dtype=torch.float32, device=dev)
+        fresh.append(states)
+    elif states is not None:
+        _check("states", states, sshape, torch.float32, dev)
+    desc = LinrecDesc(B, T, D, DTYPES[x.dtype])
+    ws, wn, keep = _linrec_workspace("linrec_fwd", desc, dev, workspace)
+    _enqueue(dev, stream, lib.delta_linrec_fwd, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(h0),
+             _addr(o), _addr(h_T), _addr(states), _addr(ws), wn, fresh=(*fresh, keep))
+    return o, h_T, states
+
+
+def linrec_bwd(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, dO: torch.Tensor,
+               beta: Optional[torch.Tensor] = None, dh_T: Optional[torch.Tensor] = None,
+               want_dh0: bool = True, stream=None, workspace: Optional[torch.Tensor] = None,
+               out: Optional[dict] = None) -> dict:
+    """Gradients of ``linrec_fwd``: dict of dx, dg, dbeta (None without beta) in x's
+    dtype and dh0 (fp32, None unless wanted).  ``states`` as ``linrec_fwd`` returned it
+    for these inputs.  ``out`` may supply any of these tensors."""
+    lib = load_library()
+    dev = _linrec_check(x, g, beta, 3)
+    B, T, D = x.shape
+    _check("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
+    _check("dO", dO, (B, T, D), x.dtype, dev)
+    if dh_T is not None:
+        _check("dh_T", dh_T, (B, D), torch.float32, dev)
+    given = dict(out or {})
+    shapes = {"dx": ((B, T, D), x.dtype), "dg": ((B, T, D), x.dtype)}
+    if beta is not None:
+        shapes["dbeta"] = ((B, T, D), x.dtype)
+    if want_dh0 or "dh0" in given:
+        shapes["dh0"] = ((B, D), torch.float32)
+    res, fresh = {"dx": None, "dg": None, "dbeta": None, "dh0": None}, []
+    for name in given:
+        if name not in shapes:
+            raise ValueError(f"{name} is not an output of this call")
+    for name, (shape, dt) in shapes.items():
+        t = given.get(name)
+        if t is None:
+            t = torch.empty(shape, dtype=dt, device=dev)
+            fresh.append(t)
+        else:
+            _check(name, t, shape, dt, dev)
+        res[name] = t
+    desc = LinrecDesc(B, T, D, DTYPES[x.dtype])
+    ws, wn, keep = _linrec_workspace("linrec_bwd", desc, dev, workspace)
+    _enqueue(dev, stream, lib.delta_linrec_bwd, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(states),
+             _addr(dO), _addr(dh_T), _addr(res["dx"]), _addr(res["dg"]), _addr(res["dbeta"]), _addr(res["dh0"]),
+             _addr(ws), wn, fresh=(*fresh, keep))
+    return res
+
+
+def linrec_step(x: torch.Tensor, g: torch.Tensor, h: torch.Tensor, beta: Optional[torch.Tensor] = None,
+                slots: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """One token per sequence of the gated linear recurrence: x, g, beta [B, D], the
+    states updated in place.  ``h`` is [B, D] fp32, or with ``slots`` ([B] int32) a pool
+    [n_pages, D] of which row b's state is page slots[b]; rows with a slot outside the
+    pool are skipped (their rows of ``o`` are not written), rows that share a page act
+    in order."""
+    lib = load_library()
+    dev = _linrec_check(x, g, beta, 2)
+    B, D = x.shape
+    if h.dim() != 2:
+        raise ValueError(f"h: expected 2 dimensions, got shape {tuple(h.shape)}")
+    _check("h", h, (B if slots is None else h.shape[0], D), torch.float32, dev)
+    if slots is not None:
+        _check("slots", slots, (B,), torch.int32, dev)
+    fresh = ()
+    if o is None:
+        o = torch.empty_like(x)
+        fresh = (o,)
+    else:
+        _check("o", o, (B, D), x.dtype, dev)
+    desc = LinrecDesc(B, 1, D, DTYPES[x.dtype])
+    _enqueue(dev, stream, lib.delta_linrec_step, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(h),
+             h.shape[0], _addr(slots), _addr(o), fresh=fresh)
+    return o
+
+
+def delta_decode_slots(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
+                       pool: torch.Tensor, slots: torch.Tensor, wgate: Optional[torch.Tensor] = None,
+                       g: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """``delta_decode`` on a pool of states [n_pages, H, dv, dk] fp32, updated in place:
+    row b's state is page slots[b] ([B] int32).  Rows with a slot outside the pool are
+    skipped (their rows of ``o`` are not written); rows that share a page act in order."""
+    lib = load_library()
+    var = VARIANTS[variant]
+    dev = _gpu("q", q)
+    if q.dim() != 3 or v.dim() != 3 or pool.dim() != 4:
+        raise ValueError("expected q [B, H_k, dk], v [B, H, dv] and pool [n_pages, H, dv, dk]")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    dt = q.dtype
+    if dt not in DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    _check("q", q, (B, Hk, dk), dt, dev)
+    _check("k", k, (B, Hk, dk), dt, dev)
+    _check("v", v, (B, H, dv), dt, dev)
+    _check("beta", beta, (B, H, dk) if variant in _CHANNEL_BETA else (B, H), dt, dev)
+    if variant == "gdn2":
+        _check("wgate", wgate, (B, H, dv), dt, dev)
+    elif wgate is not None:
+        raise ValueError("only gdn2 takes a write gate")
+    if variant == "deltanet":
+        if g is not None:
+            raise ValueError("deltanet takes no decay")
+    else:
+        _check("g", g, (B, H) if variant == "gdn" else (B, H, dk), dt, dev)
+    _check("pool", pool, (pool.shape[0], H, dv, dk), torch.float32, dev)
+    _check("slots", slots, (B,), torch.int32, dev)
+    fresh = ()
+    if o is None:
+        o = torch.empty((B, H, dv), dtype=dt, device=dev)
+        fresh = (o,)
+    else:
+        _check("o", o, (B, H, dv), dt, dev)
+    desc = DrDesc(B, 1, H, dk, dv, 64, var, DTYPES[dt], Hk)
+    _enqueue(dev, stream, lib.delta_decode_slots, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(beta),
+             _addr(wgate), _addr(g), _addr(pool), pool.shape[0], _addr(slots), _addr(o), fresh=fresh)
+    return o
+
+
+def _pool(name: str, t: torch.Tensor, dev) -> int:
+    """Floats per page of a pool [n_pages, ...]."""
+    if t.dim() < 2:
+        raise ValueError(f"{name}: expected [n_pages, ...], got shape {tuple(t.shape)}")
+    _check(name, t, t.shape, torch.float32, dev)
+    return t.numel() // t.shape[0] if t.shape[0] else 0
+
+
+def pages_copy(pool: torch.Tensor, dst: torch.Tensor, src: torch.Tensor,
+               src_pool: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Copy, fork and clear pages: entry i copies page src[i] of ``src_pool`` (None:
+    ``pool``) to page dst[i] of ``pool``, src[i] = -1 clears it.  ``pool`` [n_pages, ...]
+    fp32, ``dst`` and ``src`` [n] int32.  Entries act in order; one with another number
+    outside its pool does nothing.  Returns ``pool``."""
+    lib = load_library()
+    dev = _gpu("pool", pool)
+    page = _pool("pool", pool, dev)
+    if src_pool is None:
+        src_pool = pool
+    elif _pool("src_pool", src_pool, dev) != page:
+        raise ValueError(f"src_pool: pages of {tuple(src_pool.shape[1:])}, expected {tuple(pool.shape[1:])}")
+    n = dst.numel()
+    _check("dst", dst, (n,), torch.int32, dev)
+    _check("src", src, (n,), torch.int32, dev)
+    desc = PagesDesc(page, pool.shape[0], n)
+    _enqueue(dev, stream, lib.delta_pages_copy, ctypes.byref(desc), _addr(pool), _addr(dst), _addr(src_pool),
+             src_pool.shape[0], _addr(src))
+    return pool
+
+
+def pages_compact(pool: torch.Tensor, slots: torch.Tensor, slots_out: Optional[torch.Tensor] = None,
+                  n_live: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Move the live pages of ``pool`` [n_pages, ...] fp32 to its front, in place.
+    ``slots`` [n] int32 names the live sequences' pages (numbers outside the pool: ended
+    sequences).  Returns (slots_out [n] int32, where each page is now, -1 for ended
+    sequences; n_live [1] int32)."""
+    lib = load_library()
+    dev = _gpu("pool", pool)
+    page = _pool("pool", pool, dev)
+    n = slots.numel()
+    _check("slots", slots, (n,), torch.int32, dev)
+    fresh = []
+    if slots_out is None:
+        slots_out = torch.empty_like(slots)
+        fresh.append(slots_out)
+    else:
+        _check("slots_out", slots_out, (n,), torch.int32, dev)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=dev)
+        fresh.append(n_live)
+    else:
+        _check("n_live", n_live, (1,), torch.int32, dev)
+    desc = PagesDesc(page, pool.shape[0], n)
+    _enqueue(dev, stream, lib.delta_pages_compact, ctypes.byref(desc), _addr(pool), _addr(slots), _addr(slots_out),
+             _addr(n_live), fresh=fresh)
+    return slots_out, n_live

@@ -1,0 +1,365 @@
+"""Gated linear recurrence on the GPU against the float64 recurrence, with the bounds
+of linrecref.py: lengths and widths around the kernels' blocks, resets, long memory,
+non-finite values, in-place state, streams, captured replays, outputs' margins."""
+import pytest
+import torch
+
+import linrecref as R
+from gpu_util import announce
+from recurrent_memory_amd import ops
+from recurrent_memory_amd.autograd import linear_recurrence
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+SHAPES = [(1, 1, 1), (2, 1, 7), (3, 2, 64), (1, 15, 3), (2, 16, 130), (2, 17, 65), (1, 31, 128), (3, 33, 63),
+          (1, 127, 129), (2, 128, 8), (1, 129, 256), (2, 255, 127), (1, 256, 130), (2, 257, 1), (5, 300, 10),
+          (1, 513, 66), (2, 1000, 101), (1, 4099, 48), (70, 40, 2), (3, 777, 1001), (2, 520, 2048)]
+
+
+def _fwd_check(x, g, b, h0, want_states=True):
+    o, hT, st = ops.linrec_fwd(x, g, beta=b, h0=h0, want_states=want_states)
+    torch.cuda.synchronize()
+    h, err = R.states_and_bounds(x, g, b, h0)
+    R.check("o", o, h[:, 1:], err[:, 1:])
+    R.check("h_T", hT, h[:, -1], err[:, -1])
+    if want_states:
+        R.check("states", st, h[:, :-1:16], err[:, :-1:16])
+    return o, hT, st
+
+
+def _bwd_check(x, g, b, h0, dO, dhT, st, names=("dx", "dg", "dbeta", "dh0")):
+    gr = ops.linrec_bwd(x, g, st, dO, beta=b, dh_T=dhT)
+    torch.cuda.synchronize()
+    ref = R.grads_and_bounds(x, g, b, h0, dO, dhT)
+    for n in names:
+        if n in ref:
+            R.check(n, gr[n], *ref[n])
+    return gr
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", SHAPES)
+def test_forward_and_backward(dtype, B, T, D):
+    announce("linrec", dtype, B, T, D)
+    # both gates and states in one case, neither in the other
+    for beta, h0 in ((True, True), (False, False)):
+        x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], beta, h0, seed=B + T + D)
+        _, _, st = _fwd_check(x, g, b, s)
+        _bwd_check(x, g, b, s, dO, dhT if h0 else None, st)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D,scale", [(1, 20000, 70, 1 / 512), (2, 9000, 256, 1 / 64), (1, 33000, 33, 1 / 16)])
+def test_long_sequences(dtype, B, T, D, scale):
+    """Slow decays over many tiles: what is carried across them matters."""
+    announce("linrec_long", dtype, B, T, D, scale)
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], True, True, scale, seed=T)
+    _, _, st = _fwd_check(x, g, b, s)
+    _bwd_check(x, g, b, s, dO, dhT, st)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_resets_and_padding(dtype):
+    """g = -inf forgets everything before its token, forwards and backwards; tokens
+    with g = 0 and x = 0 leave the state as it is."""
+    announce("linrec_resets", dtype)
+    B, T, D = 2, 700, 96
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], True, True, 0.1, seed=5)
+    g[0, 0], g[1, 300], g[0, 256], g[0, 255, :10] = (-float("inf"),) * 4
+    g[1, 600:], x[1, 600:] = 0, 0
+    o, hT, st = _fwd_check(x, g, b, s)
+    gr = _bwd_check(x, g, b, s, dO, dhT, st)
+    assert bool((gr["dh0"][0] == 0).all())
+    assert bool((gr["dg"][0, 256] == 0).all())
+    # the padded tail only carries the state on
+    o2, hT2, _ = ops.linrec_fwd(x[1:, :600].contiguous(), g[1:, :600].contiguous(), beta=b[1:, :600].contiguous(), h0=s[1:])
+    assert torch.equal(o2[0], o[1, :600])
+    h600 = R.states_and_bounds(x[1:, :600], g[1:, :600], b[1:, :600], s[1:])
+    R.check("h_T", hT[1:], h600[0][:, -1], 2 * h600[1][:, -1])
+    R.check("h_T", hT2, h600[0][:, -1], h600[1][:, -1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_stays_in_its_channel(dtype, value):
+    announce("linrec_nonfinite", dtype, value)
+    x, g, b, s, dO, dhT = R.inputs(2, 600, 131, DT[dtype], True, True, 0.1, seed=6)
+    g = g.clamp(min=-0.125)                     # no decay underflows to zero within 300 tokens
+    o0, h0, st0 = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+    x1 = x.clone()
+    x1[1, 290, 77] = value
+    o1, h1, st1 = ops.linrec_fwd(x1, g, beta=b, h0=s, want_states=True)
+    torch.cuda.synchronize()
+    rest = torch.ones(2, 131, dtype=torch.bool, device="cuda")
+    rest[1, 77] = False
+    assert torch.equal(o1.transpose(1, 2)[rest], o0.transpose(1, 2)[rest]) and torch.equal(h1[rest], h0[rest])
+    assert torch.equal(o1[1, :290, 77], o0[1, :290, 77])
+    assert not bool(torch.isfinite(o1[1, 290:, 77]).any()) and not bool(torch.isfinite(h1[1, 77]))
+    dO1 = dO.clone()
+    dO1[1, 290, 77] = value
+    g0 = ops.linrec_bwd(x, g, st0, dO, beta=b, dh_T=dhT)
+    g1 = ops.linrec_bwd(x, g, st0, dO1, beta=b, dh_T=dhT)
+    torch.cuda.synchronize()
+    for n in ("dx", "dg", "dbeta"):
+        assert torch.equal(g1[n].transpose(1, 2)[rest], g0[n].transpose(1, 2)[rest]), n
+        assert torch.equal(g1[n][1, 291:, 77], g0[n][1, 291:, 77]), n
+        assert not bool(torch.isfinite(g1[n][1, :291, 77]).any()), n
+    assert torch.equal(g1["dh0"][rest], g0["dh0"][rest]) and not bool(torch.isfinite(g1["dh0"][1, 77]))
+
+
+class Margins:
+    """A tensor inside a buffer of NaN patterns, 64 KiB of them on each side."""
+
+    def __init__(self, shape, dtype):
+        self.bits = {torch.bfloat16: torch.int16, torch.float32: torch.int32, torch.uint8: torch.uint8}[dtype]
+        esz = torch.empty(0, dtype=dtype).element_size()
+        self.m, n = 65536 // esz, 1
+        for v in shape:
+            n *= v
+        self.n = n
+        self.buf = torch.empty(n + 2 * self.m, dtype=dtype, device="cuda")
+        self.buf.view(self.bits).fill_(-1 if dtype != torch.uint8 else 255)
+        self.sentinel = self.buf.view(self.bits)[0].item()
+        self.t = self.buf[self.m:self.m + n].view(shape)
+
+    def check(self, name, full=True):
+        b = self.buf.view(self.bits)
+        assert bool((b[:self.m] == self.sentinel).all()), f"{name}: written in front of it"
+        assert bool((b[self.m + self.n:] == self.sentinel).all()), f"{name}: written behind it"
+        if full:
+            assert not bool((b[self.m:self.m + self.n] == self.sentinel).any()), f"{name}: not all written"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 1), (2, 17, 65), (1, 257, 33), (2, 1000, 130), (3, 530, 77)])
+def test_writes_only_its_outputs(dtype, B, T, D):
+    announce("linrec_margins", dtype, B, T, D)
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], True, True, seed=9)
+    d = ops.LinrecDesc(B, T, D, ops.DTYPES[DT[dtype]])
+    o, hT = Margins((B, T, D), DT[dtype]), Margins((B, D), torch.float32)
+    st = Margins((B, -(-T // 16), D), torch.float32)
+    wf, wb = (Margins((max(1, ops.workspace_bytes(e, d)),), torch.uint8) for e in ("linrec_fwd", "linrec_bwd"))
+    ops.linrec_fwd(x, g, beta=b, h0=s, o=o.t, h_T=hT.t, states=st.t, workspace=wf.t)
+    out = {n: Margins((B, T, D), DT[dtype]) for n in ("dx", "dg", "dbeta")}
+    out["dh0"] = Margins((B, D), torch.float32)
+    ops.linrec_bwd(x, g, st.t, dO, beta=b, dh_T=dhT, out={n: m.t for n, m in out.items()}, workspace=wb.t)
+    torch.cuda.synchronize()
+    for n, m in dict(o=o, h_T=hT, states=st, **out).items():
+        m.check(n)
+    for n, m in (("forward workspace", wf), ("backward workspace", wb)):
+        m.check(n, full=False)
+
+
+def test_in_place_state_and_chunked_prefill():
+    """A sequence in two calls, its state updated in place, is the sequence in one."""
+    announce("linrec_chunked")
+    x, g, b, s, _, _ = R.inputs(2, 600, 130, torch.float32, True, True, 0.1, seed=10)
+    h, err = R.states_and_bounds(x, g, b, s)
+    st = s.clone()
+    for lo, hi in ((0, 1), (1, 290), (290, 600)):
+        o, hT, none = ops.linrec_fwd(x[:, lo:hi].contiguous(), g[:, lo:hi].contiguous(), beta=b[:, lo:hi].contiguous(),
+                                     h0=st, h_T=st)
+        assert hT is st and none is None
+        R.check("o", o, h[:, lo + 1:hi + 1], err[:, lo + 1:hi + 1])
+    R.check("h_T", st, h[:, -1], err[:, -1])
+    o, hT, _ = ops.linrec_fwd(x, g, beta=b, h0=s, want_state=False)
+    assert hT is None
+    R.check("o", o, h[:, 1:], err[:, 1:])
+
+
+@pytest.mark.parametrize("B,T,D", [(2, 3000, 300), (4, 100, 64)])
+def test_same_results_on_every_run(B, T, D):
+    """Bitwise, also while another stream runs the same operator."""
+    announce("linrec_deterministic", B, T, D)
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, torch.bfloat16, True, True, 0.05, seed=11)
+    o, hT, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+    gr = ops.linrec_bwd(x, g, st, dO, beta=b, dh_T=dhT)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            o1, h1, st1 = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+            gr1 = ops.linrec_bwd(x, g, st1, dO, beta=b, dh_T=dhT)
+        o2, h2, st2 = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+        gr2 = ops.linrec_bwd(x, g, st2, dO, beta=b, dh_T=dhT)
+        torch.cuda.synchronize()
+        for a, c in ((o1, o), (o2, o), (h1, hT), (h2, hT), (st1, st), (st2, st)):
+            assert torch.equal(a, c)
+        for n in gr:
+            assert torch.equal(gr1[n], gr[n]) and torch.equal(gr2[n], gr[n]), n
+
+
+def test_stream_argument():
+    announce("linrec_stream")
+    x, g, b, s, dO, _ = R.inputs(2, 700, 200, torch.float32, True, True, 0.1, seed=12)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, hT, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True, stream=side)
+    gr = ops.linrec_bwd(x, g, st, dO, beta=b, stream=side)
+    junk = [torch.full_like(x, 7.0) for _ in range(4)]      # must not land in memory still in use there
+    side.synchronize()
+    h, err = R.states_and_bounds(x, g, b, s)
+    R.check("o", o, h[:, 1:], err[:, 1:])
+    for n, (v, e) in R.grads_and_bounds(x, g, b, s, dO, None).items():
+        R.check(n, gr[n], v, e)
+    assert all(bool((j == 7.0).all()) for j in junk)
+
+
+def test_captured_and_replayed():
+    """Two graphs of the operator, replayed in turn with new inputs and eager work between."""
+    announce("linrec_graph")
+    shapes = [(2, 1100, 130), (1, 40, 64)]
+    sets, graphs = [], []
+    for i, (B, T, D) in enumerate(shapes):
+        x, g, b, s, dO, dhT = R.inputs(B, T, D, torch.float32, True, True, 0.1, seed=13 + i)
+        ops.linrec_fwd(x, g, beta=b, h0=s)
+        torch.cuda.synchronize()
+        gph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gph):
+            o, hT, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+            gr = ops.linrec_bwd(x, g, st, dO, beta=b, dh_T=dhT)
+        sets.append((x, g, b, s, dO, dhT, o, hT, gr))
+        graphs.append(gph)
+    for rep in range(3):
+        for (x, g, b, s, dO, dhT, o, hT, gr), gph in zip(sets, graphs):
+            new = R.inputs(*x.shape, torch.float32, True, True, 0.1, seed=100 + rep)
+            for a, c in zip((x, g, b, s, dO, dhT), new):
+                a.copy_(c)
+            gph.replay()
+            torch.cuda.synchronize()
+            o2, h2, st2 = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+            gr2 = ops.linrec_bwd(x, g, st2, dO, beta=b, dh_T=dhT)
+            torch.cuda.synchronize()
+            assert torch.equal(o, o2) and torch.equal(hT, h2), rep
+            for n in gr:
+                assert torch.equal(gr[n], gr2[n]), (rep, n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("with_beta,with_h0", [(True, True), (False, True), (True, False)])
+def test_autograd(dtype, with_beta, with_h0):
+    announce("linrec_autograd", dtype, with_beta, with_h0)
+    x, g, b, s, dO, dhT = R.inputs(2, 300, 70, DT[dtype], with_beta, with_h0, 0.3, seed=20)
+    leaves = [t.requires_grad_(True) for t in (x, g, b, s) if t is not None]
+    o, hT = linear_recurrence(x, g, b, s)
+    grads = torch.autograd.grad((o, hT), leaves, (dO, dhT))
+    ref = R.grads_and_bounds(*(None if t is None else t.detach() for t in (x, g, b, s)), dO, dhT)
+    names = ["dx", "dg"] + (["dbeta"] if with_beta else []) + (["dh0"] if with_h0 else [])
+    for n, got in zip(names, grads):
+        R.check(n, got, *ref[n])
+    # one of the two outputs used, with a gradient in another layout
+    o, hT = linear_recurrence(x, g, b, s)
+    w = dO.transpose(0, 1).contiguous().transpose(0, 1)
+    (gx,) = torch.autograd.grad(o, [x], w)
+    R.check("dx", gx, *R.grads_and_bounds(*(None if t is None else t.detach() for t in (x, g, b, s)), dO, None)["dx"])
+    # no gradient wanted: nothing kept
+    with torch.no_grad():
+        o, _ = linear_recurrence(x, g, b, s)
+    assert not o.requires_grad
+
+
+def test_more_than_2_to_the_31_elements():
+    """Offsets past 32 bits: the last tokens of two sequences of 2^30 + elements each,
+    whose states follow from the last reset."""
+    B, T, D = 2, 16500, 65600                   # 2.16e9 elements
+    announce("linrec_large", B, T, D)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x = torch.randn(B, T, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    g = torch.full_like(x, -0.125)
+    g[:, T - 300] = -float("inf")
+    o, hT, st = ops.linrec_fwd(x, g, want_states=True)
+    cols = torch.tensor([0, 1, 64, 127, 128, 65599], device="cuda")
+    tail = lambda t: t[:, T - 300:, cols].contiguous()      # noqa: E731
+    h, err = R.states_and_bounds(tail(x), tail(g), None, None)
+    R.check("o", tail(o), h[:, 1:], err[:, 1:])
+    R.check("h_T", hT[:, cols], h[:, -1], err[:, -1])
+    gr = ops.linrec_bwd(x, g, st, o)
+    ref = R.grads_and_bounds(tail(x), tail(g), None, None, tail(o), None)
+    R.check("dx", tail(gr["dx"]), *ref["dx"])
+    R.check("dg", tail(gr["dg"]), *ref["dg"])
+    del gr, st
+    torch.cuda.synchronize()
+
+
+# ---- one token at a time ----
+
+def _step_ref(x, g, b, pool, slots):
+    """fp64 states after the rows' tokens in order, the outputs, and bounds for both."""
+    h, err, o, oerr = pool.double().clone(), torch.zeros_like(pool, dtype=torch.float64), {}, {}
+    for r, page in enumerate(slots):
+        if 0 <= page < pool.shape[0]:
+            bb = None if b is None else b[r][None, None]
+            st, e = R.states_and_bounds(x[r][None, None], g[r][None, None], bb, h[page][None])
+            h[page], err[page] = st[0, 1], e[0, 1] + g[r].double().exp() * err[page]
+            o[r], oerr[r] = h[page].clone(), err[page].clone()
+    return h, err, o, oerr
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,D,slots", [
+    (3, 3, 1, None), (5, 5, 64, None), (2, 2, 2050, None), (1, 1, 1001, None),
+    (4, 9, 130, [8, 0, 3, 5]),
+    (6, 4, 260, [-1, 2, 4, 0, -7, 3]),                       # padding and numbers outside the pool
+    (7, 3, 65, [1, 1, 2, 1, 0, 2, 1]),                       # pages shared by several rows
+    (300, 280, 12, [(7 * i) % 290 - 5 for i in range(300)]),
+])
+def test_step(dtype, B, N, D, slots):
+    announce("linrec_step", dtype, B, N, D)
+    for beta in (True, False):
+        x, g, b, _, dO, _ = R.inputs(B, 1, D, DT[dtype], beta, False, seed=B + N)
+        x, g, b = x[:, 0], g[:, 0], None if b is None else b[:, 0]
+        pool = torch.randn(N, D, generator=torch.Generator().manual_seed(3)).cuda()
+        st = None if slots is None else torch.tensor(slots, dtype=torch.int32, device="cuda")
+        at = list(range(B)) if slots is None else slots
+        h, err, o, oerr = _step_ref(x, g, b, pool, at)
+        got, out = Margins((N, D), torch.float32), Margins((B, D), DT[dtype])
+        got.t.copy_(pool)
+        ops.linrec_step(x, g, got.t, beta=b, slots=st, o=out.t)
+        torch.cuda.synchronize()
+        R.check("h", got.t, h, err)
+        for r in range(B):
+            if r in o:
+                R.check("o", out.t[r], o[r], oerr[r])
+            else:
+                assert bool((out.t[r].view(out.bits) == out.sentinel).all()), f"row {r} of o was written"
+        untouched = [p for p in range(N) if p not in at]
+        assert torch.equal(got.t[untouched], pool[untouched])
+        got.check("pool")
+        out.check("o", full=False)
+
+
+def test_step_follows_the_sequence_form():
+    announce("linrec_step_sequence")
+    x, g, b, s, _, _ = R.inputs(3, 20, 70, torch.float32, True, True, 0.2, seed=30)
+    o, hT, _ = ops.linrec_fwd(x, g, beta=b, h0=s)
+    h = s.clone()
+    for t in range(20):
+        ot = ops.linrec_step(x[:, t].contiguous(), g[:, t].contiguous(), h, beta=b[:, t].contiguous())
+        R.check("o", ot, *(v[:, t + 1] for v in R.states_and_bounds(x, g, b, s)))
+    R.check("h", h, *(v[:, -1] for v in R.states_and_bounds(x, g, b, s)))
+
+
+def test_refusals():
+    x, g, b, s, dO, _ = R.inputs(2, 5, 8, torch.float32, seed=1)
+    bad = [
+        (lambda: ops.linrec_fwd(x, g[:, :4]), ValueError), (lambda: ops.linrec_fwd(x, g.bfloat16()), ValueError),
+        (lambda: ops.linrec_fwd(x.half(), g.half()), ValueError), (lambda: ops.linrec_fwd(x.transpose(0, 1), g), ValueError),
+        (lambda: ops.linrec_fwd(x.transpose(0, 1), g.transpose(0, 1)), ValueError),
+        (lambda: ops.linrec_fwd(x, g, h0=s.bfloat16()), ValueError), (lambda: ops.linrec_fwd(x, g.cpu()), ValueError),
+        (lambda: ops.linrec_fwd(x, g, o=x), ops.DeltaRuleError), (lambda: ops.linrec_fwd(x[:, :0], g[:, :0]), ops.DeltaRuleError),
+        (lambda: ops.linrec_bwd(x, g, s, dO), ValueError),
+        (lambda: ops.linrec_bwd(x, g, s[:, None], dO, out=dict(dbeta=x)), ValueError),
+        (lambda: ops.linrec_step(x[:, 0].contiguous(), g[:, 0].contiguous(), s[:1]), ValueError),
+        (lambda: ops.linrec_step(x[:, 0].contiguous(), g[:, 0].contiguous(), s, slots=torch.zeros(2, device="cuda")), ValueError),
+        (lambda: ops.linrec_fwd(x, g, stream=5), AttributeError),
+    ]
+    for i, (call, err) in enumerate(bad):
+        with pytest.raises(err):
+            call()
+            raise AssertionError(f"case {i} was taken")
+    big = torch.zeros(33, device="cuda")
+    with pytest.raises(ops.DeltaRuleError) as e:                       # 4 bytes past a multiple of 16
+        ops.linrec_fwd(big[1:].view(1, 4, 8), big[:32].view(1, 4, 8).clone())
+    assert e.value.status == 4
