@@ -10,6 +10,7 @@ import-time loader raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -440,24 +441,41 @@ def ttt_pre(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bet
 
 
 # ---- gated linear recurrence and pool of state pages (include/deltarule_ext.h) ----
+#
+# A token step takes a few microseconds on the GPU, so these bindings keep the host's
+# share small: one comparison per property on the way through, the words of a refusal
+# only when one fails.
+
+def _need(name, t, shape, dtype, dev):
+    """_check, written for tensors that pass it."""
+    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        _check(name, t, shape, dtype, dev)
+
 
 def _gpu(name: str, t: torch.Tensor) -> torch.device:
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: expected a GPU tensor, got device {t.device}")
     return t.device
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _enqueue(dev: torch.device, stream, fn, *args, fresh=()):
     """Call ``fn(*args, stream)`` with ``dev`` current, on ``stream`` or else the
     device's current stream.  ``fresh``: tensors allocated for this call, marked as
-    used on ``stream`` when that is another one than the current."""
-    if dev.index != torch.cuda.current_device():
+    used on ``stream`` if one is given."""
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _enqueue(dev, stream, fn, *args, fresh=fresh)
     if stream is None:
-        handle = torch.cuda.current_stream().cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
     else:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
@@ -474,30 +492,36 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _linrec_workspace(entry: str, desc: LinrecDesc, dev, workspace: Optional[torch.Tensor]):
-    """(workspace tensor or None, its bytes, the tensor if allocated here)."""
-    need = workspace_bytes(entry, desc)
+@functools.lru_cache(maxsize=1024)
+def _linrec_bytes(entry: str, B: int, T: int, D: int, code: int) -> int:
+    return workspace_bytes(entry, LinrecDesc(B, T, D, code))
+
+
+def _linrec_workspace(need: int, dev, workspace: Optional[torch.Tensor]):
+    """(address or None, bytes, the tensor if allocated here)."""
     if need == 0:
         return None, 0, None
     if workspace is None:
         fresh = torch.empty(need, dtype=torch.uint8, device=dev)
-        return fresh, need, fresh
+        return fresh.data_ptr(), need, fresh
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the call's device")
-    return workspace, workspace.numel() * workspace.element_size(), None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
 
 
 def _linrec_check(x, g, beta, dims: int):
+    """(device, shape, dtype, its code) of the inputs."""
     dev = _gpu("x", x)
-    if x.dim() != dims:
-        raise ValueError(f"x: expected {dims} dimensions, got shape {tuple(x.shape)}")
-    if x.dtype not in DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    _check("x", x, x.shape, x.dtype, dev)
-    _check("g", g, x.shape, x.dtype, dev)
+    shape, dt = x.shape, x.dtype
+    if len(shape) != dims:
+        raise ValueError(f"x: expected {dims} dimensions, got shape {tuple(shape)}")
+    code = _dtype_code(x)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _need("g", g, shape, dt, dev)
     if beta is not None:
-        _check("beta", beta, x.shape, x.dtype, dev)
-    return dev
+        _need("beta", beta, shape, dt, dev)
+    return dev, shape, dt, code
 
 
 def linrec_fwd(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
@@ -514,32 +538,30 @@ def linrec_fwd(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = 
     needs (None unless wanted or given), [B, ceil(T / LINREC_BLOCK), D] fp32.
     """
     lib = load_library()
-    dev = _linrec_check(x, g, beta, 3)
-    B, T, D = x.shape
+    dev, shape, dt, code = _linrec_check(x, g, beta, 3)
+    B, T, D = shape
     if h0 is not None:
-        _check("h0", h0, (B, D), torch.float32, dev)
-    fresh = []
+        _need("h0", h0, (B, D), torch.float32, dev)
+    new_o = new_h = new_s = None
     if o is None:
-        o = torch.empty_like(x)
-        fresh.append(o)
+        o = new_o = torch.empty_like(x)
     else:
-        _check("o", o, (B, T, D), x.dtype, dev)
-    if h_T is None and want_state:
-        h_T = torch.empty((B, D), dtype=torch.float32, device=dev)
-        fresh.append(h_T)
-    elif h_T is not None:
-        _check("h_T", h_T, (B, D), torch.float32, dev)
-    sshape = (B, -(-T // LINREC_BLOCK), D)
-    if states is None and want_states:
-        states = torch.empty(sshape, dtype=torch.float32, device=dev)
-        fresh.append(states)
-    elif states is not None:
-        _check("states", states, sshape, torch.float32, dev)
-    desc = LinrecDesc(B, T, D, DTYPES[x.dtype])
-    ws, wn, keep = _linrec_workspace("linrec_fwd", desc, dev, workspace)
-    _enqueue(dev, stream, lib.delta_linrec_fwd, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(h0),
-             _addr(o), _addr(h_T), _addr(states), _addr(ws), wn, fresh=(*fresh, keep))
+        _need("o", o, shape, dt, dev)
+    if h_T is not None:
+        _need("h_T", h_T, (B, D), torch.float32, dev)
+    elif want_state:
+        h_T = new_h = torch.empty((B, D), dtype=torch.float32, device=dev)
+    if states is not None:
+        _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
+    elif want_states:
+        states = new_s = torch.empty((B, -(-T // LINREC_BLOCK), D), dtype=torch.float32, device=dev)
+    ws, wn, keep = _linrec_workspace(_linrec_bytes("linrec_fwd", B, T, D, code), dev, workspace)
+    _enqueue(dev, stream, lib.delta_linrec_fwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+             _addr(h0), o.data_ptr(), _addr(h_T), _addr(states), ws, wn, fresh=(new_o, new_h, new_s, keep))
     return o, h_T, states
+
+
+_LINREC_GRADS = ("dx", "dg", "dbeta", "dh0")
 
 
 def linrec_bwd(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, dO: torch.Tensor,
@@ -550,35 +572,34 @@ def linrec_bwd(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, dO: torch
     dtype and dh0 (fp32, None unless wanted).  ``states`` as ``linrec_fwd`` returned it
     for these inputs.  ``out`` may supply any of these tensors."""
     lib = load_library()
-    dev = _linrec_check(x, g, beta, 3)
-    B, T, D = x.shape
-    _check("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
-    _check("dO", dO, (B, T, D), x.dtype, dev)
+    dev, shape, dt, code = _linrec_check(x, g, beta, 3)
+    B, T, D = shape
+    _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
+    _need("dO", dO, shape, dt, dev)
     if dh_T is not None:
-        _check("dh_T", dh_T, (B, D), torch.float32, dev)
-    given = dict(out or {})
-    shapes = {"dx": ((B, T, D), x.dtype), "dg": ((B, T, D), x.dtype)}
-    if beta is not None:
-        shapes["dbeta"] = ((B, T, D), x.dtype)
-    if want_dh0 or "dh0" in given:
-        shapes["dh0"] = ((B, D), torch.float32)
-    res, fresh = {"dx": None, "dg": None, "dbeta": None, "dh0": None}, []
+        _need("dh_T", dh_T, (B, D), torch.float32, dev)
+    given = out or {}
     for name in given:
-        if name not in shapes:
+        if name not in _LINREC_GRADS or (name == "dbeta" and beta is None):
             raise ValueError(f"{name} is not an output of this call")
-    for name, (shape, dt) in shapes.items():
+    res, fresh = {}, []
+    for name in _LINREC_GRADS:
         t = given.get(name)
-        if t is None:
-            t = torch.empty(shape, dtype=dt, device=dev)
+        if t is not None:
+            _need(name, t, (B, D) if name == "dh0" else shape, torch.float32 if name == "dh0" else dt, dev)
+        elif name == "dh0":
+            if want_dh0:
+                t = torch.empty((B, D), dtype=torch.float32, device=dev)
+                fresh.append(t)
+        elif name != "dbeta" or beta is not None:
+            t = torch.empty_like(x)
             fresh.append(t)
-        else:
-            _check(name, t, shape, dt, dev)
         res[name] = t
-    desc = LinrecDesc(B, T, D, DTYPES[x.dtype])
-    ws, wn, keep = _linrec_workspace("linrec_bwd", desc, dev, workspace)
-    _enqueue(dev, stream, lib.delta_linrec_bwd, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(states),
-             _addr(dO), _addr(dh_T), _addr(res["dx"]), _addr(res["dg"]), _addr(res["dbeta"]), _addr(res["dh0"]),
-             _addr(ws), wn, fresh=(*fresh, keep))
+    ws, wn, keep = _linrec_workspace(_linrec_bytes("linrec_bwd", B, T, D, code), dev, workspace)
+    fresh.append(keep)
+    _enqueue(dev, stream, lib.delta_linrec_bwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+             states.data_ptr(), dO.data_ptr(), _addr(dh_T), res["dx"].data_ptr(), res["dg"].data_ptr(),
+             _addr(res["dbeta"]), _addr(res["dh0"]), ws, wn, fresh=fresh)
     return res
 
 
@@ -591,22 +612,22 @@ def linrec_step(x: torch.Tensor, g: torch.Tensor, h: torch.Tensor, beta: Optiona
     pool are skipped (their rows of ``o`` are not written), rows that share a page act
     in order."""
     lib = load_library()
-    dev = _linrec_check(x, g, beta, 2)
-    B, D = x.shape
+    dev, shape, dt, code = _linrec_check(x, g, beta, 2)
+    B, D = shape
     if h.dim() != 2:
         raise ValueError(f"h: expected 2 dimensions, got shape {tuple(h.shape)}")
-    _check("h", h, (B if slots is None else h.shape[0], D), torch.float32, dev)
+    pages = h.shape[0]
+    _need("h", h, (B if slots is None else pages, D), torch.float32, dev)
     if slots is not None:
-        _check("slots", slots, (B,), torch.int32, dev)
+        _need("slots", slots, (B,), torch.int32, dev)
     fresh = ()
     if o is None:
         o = torch.empty_like(x)
         fresh = (o,)
     else:
-        _check("o", o, (B, D), x.dtype, dev)
-    desc = LinrecDesc(B, 1, D, DTYPES[x.dtype])
-    _enqueue(dev, stream, lib.delta_linrec_step, ctypes.byref(desc), _addr(x), _addr(g), _addr(beta), _addr(h),
-             h.shape[0], _addr(slots), _addr(o), fresh=fresh)
+        _need("o", o, shape, dt, dev)
+    _enqueue(dev, stream, lib.delta_linrec_step, LinrecDesc(B, 1, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+             h.data_ptr(), pages, _addr(slots), o.data_ptr(), fresh=fresh)
     return o
 
 
@@ -624,42 +645,42 @@ def delta_decode_slots(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.
         raise ValueError("expected q [B, H_k, dk], v [B, H, dv] and pool [n_pages, H, dv, dk]")
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
-    dt = q.dtype
-    if dt not in DTYPES:
-        raise ValueError(f"unsupported dtype {dt}")
-    _check("q", q, (B, Hk, dk), dt, dev)
-    _check("k", k, (B, Hk, dk), dt, dev)
-    _check("v", v, (B, H, dv), dt, dev)
-    _check("beta", beta, (B, H, dk) if variant in _CHANNEL_BETA else (B, H), dt, dev)
+    dt, code = q.dtype, _dtype_code(q)
+    _need("q", q, (B, Hk, dk), dt, dev)
+    _need("k", k, (B, Hk, dk), dt, dev)
+    _need("v", v, (B, H, dv), dt, dev)
+    _need("beta", beta, (B, H, dk) if variant in _CHANNEL_BETA else (B, H), dt, dev)
     if variant == "gdn2":
-        _check("wgate", wgate, (B, H, dv), dt, dev)
+        _need("wgate", wgate, (B, H, dv), dt, dev)
     elif wgate is not None:
         raise ValueError("only gdn2 takes a write gate")
     if variant == "deltanet":
         if g is not None:
             raise ValueError("deltanet takes no decay")
     else:
-        _check("g", g, (B, H) if variant == "gdn" else (B, H, dk), dt, dev)
-    _check("pool", pool, (pool.shape[0], H, dv, dk), torch.float32, dev)
-    _check("slots", slots, (B,), torch.int32, dev)
+        _need("g", g, (B, H) if variant == "gdn" else (B, H, dk), dt, dev)
+    pages = pool.shape[0]
+    _need("pool", pool, (pages, H, dv, dk), torch.float32, dev)
+    _need("slots", slots, (B,), torch.int32, dev)
     fresh = ()
     if o is None:
         o = torch.empty((B, H, dv), dtype=dt, device=dev)
         fresh = (o,)
     else:
-        _check("o", o, (B, H, dv), dt, dev)
-    desc = DrDesc(B, 1, H, dk, dv, 64, var, DTYPES[dt], Hk)
-    _enqueue(dev, stream, lib.delta_decode_slots, ctypes.byref(desc), _addr(q), _addr(k), _addr(v), _addr(beta),
-             _addr(wgate), _addr(g), _addr(pool), pool.shape[0], _addr(slots), _addr(o), fresh=fresh)
+        _need("o", o, (B, H, dv), dt, dev)
+    _enqueue(dev, stream, lib.delta_decode_slots, DrDesc(B, 1, H, dk, dv, 64, var, code, Hk), q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), beta.data_ptr(), _addr(wgate), _addr(g), pool.data_ptr(), pages,
+             slots.data_ptr(), o.data_ptr(), fresh=fresh)
     return o
 
 
-def _pool(name: str, t: torch.Tensor, dev) -> int:
+def _page(name: str, t: torch.Tensor, dev) -> int:
     """Floats per page of a pool [n_pages, ...]."""
-    if t.dim() < 2:
-        raise ValueError(f"{name}: expected [n_pages, ...], got shape {tuple(t.shape)}")
-    _check(name, t, t.shape, torch.float32, dev)
-    return t.numel() // t.shape[0] if t.shape[0] else 0
+    shape = t.shape
+    if len(shape) < 2:
+        raise ValueError(f"{name}: expected [n_pages, ...], got shape {tuple(shape)}")
+    _need(name, t, shape, torch.float32, dev)
+    return t.numel() // shape[0] if shape[0] else 0
 
 
 def pages_copy(pool: torch.Tensor, dst: torch.Tensor, src: torch.Tensor,
@@ -670,17 +691,16 @@ def pages_copy(pool: torch.Tensor, dst: torch.Tensor, src: torch.Tensor,
     outside its pool does nothing.  Returns ``pool``."""
     lib = load_library()
     dev = _gpu("pool", pool)
-    page = _pool("pool", pool, dev)
+    page = _page("pool", pool, dev)
     if src_pool is None:
         src_pool = pool
-    elif _pool("src_pool", src_pool, dev) != page:
+    elif _page("src_pool", src_pool, dev) != page:
         raise ValueError(f"src_pool: pages of {tuple(src_pool.shape[1:])}, expected {tuple(pool.shape[1:])}")
     n = dst.numel()
-    _check("dst", dst, (n,), torch.int32, dev)
-    _check("src", src, (n,), torch.int32, dev)
-    desc = PagesDesc(page, pool.shape[0], n)
-    _enqueue(dev, stream, lib.delta_pages_copy, ctypes.byref(desc), _addr(pool), _addr(dst), _addr(src_pool),
-             src_pool.shape[0], _addr(src))
+    _need("dst", dst, (n,), torch.int32, dev)
+    _need("src", src, (n,), torch.int32, dev)
+    _enqueue(dev, stream, lib.delta_pages_copy, PagesDesc(page, pool.shape[0], n), pool.data_ptr(), dst.data_ptr(),
+             src_pool.data_ptr(), src_pool.shape[0], src.data_ptr())
     return pool
 
 
@@ -692,21 +712,18 @@ def pages_compact(pool: torch.Tensor, slots: torch.Tensor, slots_out: Optional[t
     sequences; n_live [1] int32)."""
     lib = load_library()
     dev = _gpu("pool", pool)
-    page = _pool("pool", pool, dev)
+    page = _page("pool", pool, dev)
     n = slots.numel()
-    _check("slots", slots, (n,), torch.int32, dev)
-    fresh = []
+    _need("slots", slots, (n,), torch.int32, dev)
+    new_s = new_n = None
     if slots_out is None:
-        slots_out = torch.empty_like(slots)
-        fresh.append(slots_out)
+        slots_out = new_s = torch.empty_like(slots)
     else:
-        _check("slots_out", slots_out, (n,), torch.int32, dev)
+        _need("slots_out", slots_out, (n,), torch.int32, dev)
     if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=dev)
-        fresh.append(n_live)
+        n_live = new_n = torch.empty(1, dtype=torch.int32, device=dev)
     else:
-        _check("n_live", n_live, (1,), torch.int32, dev)
-    desc = PagesDesc(page, pool.shape[0], n)
-    _enqueue(dev, stream, lib.delta_pages_compact, ctypes.byref(desc), _addr(pool), _addr(slots), _addr(slots_out),
-             _addr(n_live), fresh=fresh)
+        _need("n_live", n_live, (1,), torch.int32, dev)
+    _enqueue(dev, stream, lib.delta_pages_compact, PagesDesc(page, pool.shape[0], n), pool.data_ptr(),
+             slots.data_ptr(), slots_out.data_ptr(), n_live.data_ptr(), fresh=(new_s, new_n))
     return slots_out, n_live
