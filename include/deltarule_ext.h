@@ -96,7 +96,8 @@ dr_status delta_linrec_bwd(const dr_linrec_desc* desc, const void* x, const void
  *
  * A pool is n_pages pages of `page` floats each; a page holds the state of one
  * sequence: [H, d_v, d_k] of the delta rule, [D] of the linear recurrence.
- * Sequences name their pages by slot numbers (int32, device memory).
+ * Sequences name their pages by slot numbers: lists of int32 in device memory,
+ * which need be aligned to 4 bytes only.
  */
 #define DR_MAX_PAGES 65536
 

@@ -56,6 +56,9 @@ dr_status check_pages_desc(const dr_pages_desc* d) {
     return DR_OK;
 }
 
+// Lists of page numbers may start at any int32 (a part of a longer list).
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 dr_status launched(hipError_t e) { return e == hipSuccess ? DR_OK : DR_E_LAUNCH; }
 
 }  // namespace
@@ -167,9 +170,10 @@ dr_status delta_linrec_step(const dr_linrec_desc* desc, const void* x, const voi
         if (st != DR_OK) return st;
         if (x == nullptr || g == nullptr || h == nullptr || o == nullptr) return DR_E_NULLPTR;
         if (n_pages < 1 || (slots == nullptr ? n_pages != desc->B : n_pages > DR_MAX_PAGES)) return DR_E_SHAPE;
-        const void* ptrs[] = {x, g, beta, h, slots, o};
+        const void* ptrs[] = {x, g, beta, h, o};
         for (const void* p : ptrs)
             if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;
+        if (!aligned4(slots)) return DR_E_ALIGN;
         const int64_t eb = desc->dtype == DR_F32 ? 4 : 2;
         const Span in[] = {span_of(x, sz.row, eb), span_of(g, sz.row, eb), span_of(beta, sz.row, eb),
                            span_of(slots, desc->B, 4)};
@@ -199,9 +203,10 @@ dr_status delta_decode_slots(const dr_desc* desc, const void* q, const void* k, 
         st = check_gate_ptrs(desc, beta, wgate, g);
         if (st != DR_OK) return st;
         if (n_pages < 1 || n_pages > DR_MAX_PAGES) return DR_E_SHAPE;
-        const void* ptrs[] = {q, k, v, beta, wgate, g, pool, slots, o};
+        const void* ptrs[] = {q, k, v, beta, wgate, g, pool, o};
         for (const void* p : ptrs)
             if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;
+        if (!aligned4(slots)) return DR_E_ALIGN;
         const int64_t eb = desc->dtype == DR_F32 ? 4 : 2;
         const int64_t page = static_cast<int64_t>(desc->H) * desc->d_v * desc->d_k;
         const Span in[] = {span_of(q, sz.qk, eb),        span_of(k, sz.qk, eb), span_of(v, sz.v, eb),
@@ -233,9 +238,7 @@ dr_status delta_pages_copy(const dr_pages_desc* desc, float* pool, const int32_t
         if (src_pages < 1 || src_pages > DR_MAX_PAGES || desc->page > (int64_t(1) << 40) / src_pages)
             return DR_E_SHAPE;
         if (src_pool == pool && src_pages != desc->n_pages) return DR_E_SHAPE;
-        const void* ptrs[] = {pool, src_pool, dst, src};
-        for (const void* p : ptrs)
-            if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;
+        if (!aligned16(pool) || !aligned16(src_pool) || !aligned4(dst) || !aligned4(src)) return DR_E_ALIGN;
         const Span in[] = {span_of(src_pool, desc->page * src_pages, 4), span_of(dst, desc->n, 4),
                            span_of(src, desc->n, 4)};
         const Span out[] = {span_of(pool, desc->page * desc->n_pages, 4)};
@@ -259,9 +262,7 @@ dr_status delta_pages_compact(const dr_pages_desc* desc, float* pool, const int3
         if (st != DR_OK) return st;
         if (pool == nullptr || n_live == nullptr) return DR_E_NULLPTR;
         if (desc->n > 0 && (slots == nullptr || slots_out == nullptr)) return DR_E_NULLPTR;
-        const void* ptrs[] = {pool, slots, slots_out, n_live};
-        for (const void* p : ptrs)
-            if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;
+        if (!aligned16(pool) || !aligned4(slots) || !aligned4(slots_out) || !aligned4(n_live)) return DR_E_ALIGN;
         const Span in[] = {span_of(slots, desc->n, 4)};
         const Span out[] = {span_of(pool, desc->page * desc->n_pages, 4), span_of(slots_out, desc->n, 4),
                             span_of(n_live, 1, 4)};

@@ -31,10 +31,31 @@ namespace dr {
 
 constexpr int kDecodeThreads = 256;
 
+// N consecutive floats of a state row, optionally non-temporal.
+template <int N, bool NT>
+__device__ __forceinline__ void load_state(const float* p, float* f) {
+    typedef float Vec __attribute__((ext_vector_type(N)));
+    Vec v;
+    if constexpr (NT) v = __builtin_nontemporal_load(reinterpret_cast<const Vec*>(p));
+    else v = *reinterpret_cast<const Vec*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = v[i];
+}
+template <int N, bool NT>
+__device__ __forceinline__ void store_state(float* p, const float* f) {
+    typedef float Vec __attribute__((ext_vector_type(N)));
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = f[i];
+    if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<Vec*>(p));
+    else *reinterpret_cast<Vec*>(p) = v;
+}
+
 // Token step of one row: bh = b * H + h indexes the per-token operands and o, S
 // is that head's state matrix.  Called by all kDecodeThreads threads; a thread
-// reads and writes the same elements of S in every call.
-template <int VAR, typename E, int DK, int DV>
+// reads and writes the same elements of S in every call.  NT: non-temporal accesses
+// to S.
+template <int VAR, typename E, int DK, int DV, bool NT = false>
 __device__ __forceinline__ void decode_row(const DecodeArgs& p, int bh, float* S) {
     constexpr int CPL = DK / 32;       // key columns per lane
     constexpr int RPG = DV / 8;        // rows per 32-lane group
@@ -69,13 +90,7 @@ __device__ __forceinline__ void decode_row(const DecodeArgs& p, int bh, float* S
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const float* row = S + static_cast<int64_t>(grp + 8 * j) * DK + c0;
-        if constexpr (CPL == 4) {
-            float4 x = *reinterpret_cast<const float4*>(row);
-            st[j][0] = x.x; st[j][1] = x.y; st[j][2] = x.z; st[j][3] = x.w;
-        } else {
-            float2 x = *reinterpret_cast<const float2*>(row);
-            st[j][0] = x.x; st[j][1] = x.y;
-        }
+        load_state<CPL, NT>(row, st[j]);
     }
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
@@ -173,11 +188,7 @@ __device__ __forceinline__ void decode_row(const DecodeArgs& p, int bh, float* S
                 else if constexpr (VAR == 4) out[c] = st[j][c] + u * bk[c];
                 else out[c] = st[j][c] + u * kk[c];
             }
-            if constexpr (CPL == 4) {
-                *reinterpret_cast<float4*>(row) = make_float4(out[0], out[1], out[2], out[3]);
-            } else {
-                *reinterpret_cast<float2*>(row) = make_float2(out[0], out[1]);
-            }
+            store_state<CPL, NT>(row, out);
         }
     }
 }

@@ -4,48 +4,60 @@
 // The work and the bound are the dense kernel's (8 bytes of HBM traffic per state
 // element): one workgroup per (row, head), and decode_row() does the step.  What
 // is added is one dependent load (the slot, before the state's address is known)
-// and, beside the state's own loads, a scan of the slot list for rows that share
-// the page: the first of them takes the others' tokens too, in order, so that two
-// workgroups never touch one state and a page named twice gets its two tokens one
-// after the other.
+// and a scan of the slot list for rows that share the page: the first of them takes
+// the others' tokens too, in order, so that two workgroups never touch one state and
+// a page named twice gets its two tokens one after the other.
 #include "decode_row.h"
 #include "slots.h"
 
 namespace dr {
 namespace {
 
-template <int VAR, typename E, int DK, int DV>
-__global__ __launch_bounds__(kDecodeThreads) void decode_slots_kernel(DecodeArgs p, int n_pages,
+// Four waves a SIMD, as the dense kernel has: the compiler gives the forms with a vector
+// of decays or steps (2, 4) a few registers too many by itself (64 rows of 16 heads,
+// channel-wise decay: 26 us with three waves, 23 us with four).
+template <int VAR, typename E, int DK, int DV, bool NT>
+__global__ __launch_bounds__(kDecodeThreads, VAR == 2 || VAR == 4 ? 4 : 1) void decode_slots_kernel(DecodeArgs p, int n_pages,
                                                                       const int* slots) {
     const int h = blockIdx.x % p.H;
     int b = blockIdx.x / p.H;
-    const int slot = slots[b];
-    if (slot < 0 || slot >= n_pages) return;   // padding row: nothing read, nothing written
     bool earlier, later;
-    slot_sharers(slots, p.B, b, slot, &earlier, &later);
-    if (earlier) return;
+    const int slot = slot_of_row(slots, p.B, b, &earlier, &later);
+    if (slot < 0 || slot >= n_pages || earlier) return;   // padding rows: nothing read, nothing written
     float* S = p.S + (static_cast<int64_t>(slot) * p.H + h) * DV * DK;
-    decode_row<VAR, E, DK, DV>(p, b * p.H + h, S);
-    while (later) {
-        b = next_sharer(slots, p.B, b, slot);
-        if (b == p.B) break;
-        decode_row<VAR, E, DK, DV>(p, b * p.H + h, S);
-    }
+    do {
+        // taken as new in every turn, so that the rows' addresses are not kept in registers
+        // from one to the next (145 instead of 124, one wave less on each SIMD)
+        asm volatile("" : "+s"(S));
+        decode_row<VAR, E, DK, DV, NT>(p, b * p.H + h, S);
+        if (later) b = next_sharer(slots, p.B, b, slot);
+    } while (later && b < p.B);
+}
+
+// From half of the last-level cache on, the states of a call will not be there at the
+// next token, and non-temporal accesses stream them faster: 128 MiB of states 55 us
+// against 63 us plain, 256 MiB 107 against 116 us (other layers' states between the
+// tokens).  Smaller ones may still be there, if little else runs between: 64 MiB of
+// states 23 us non-temporal, 21 us plain.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
+template <int VAR, typename E, int DK, int DV>
+hipError_t launch_widths(const DecodeArgs& a, int n_pages, const int* slots, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H));
+    const dim3 block(kDecodeThreads);
+    if (static_cast<int64_t>(a.B) * a.H * DK * DV * 4 >= kStreamBytes)
+        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, DK, DV, true>), grid, block, 0, s, a, n_pages, slots);
+    else
+        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, DK, DV, false>), grid, block, 0, s, a, n_pages, slots);
+    return hipGetLastError();
 }
 
 template <int VAR, typename E>
 hipError_t launch_dims(const DecodeArgs& a, int n_pages, const int* slots, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H));
-    const dim3 block(kDecodeThreads);
-    if (a.dk == 128 && a.dv == 128)
-        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, 128, 128>), grid, block, 0, s, a, n_pages, slots);
-    else if (a.dk == 128 && a.dv == 64)
-        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, 128, 64>), grid, block, 0, s, a, n_pages, slots);
-    else if (a.dk == 64 && a.dv == 128)
-        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, 64, 128>), grid, block, 0, s, a, n_pages, slots);
-    else
-        hipLaunchKernelGGL((decode_slots_kernel<VAR, E, 64, 64>), grid, block, 0, s, a, n_pages, slots);
-    return hipGetLastError();
+    if (a.dk == 128 && a.dv == 128) return launch_widths<VAR, E, 128, 128>(a, n_pages, slots, s);
+    if (a.dk == 128) return launch_widths<VAR, E, 128, 64>(a, n_pages, slots, s);
+    if (a.dv == 128) return launch_widths<VAR, E, 64, 128>(a, n_pages, slots, s);
+    return launch_widths<VAR, E, 64, 64>(a, n_pages, slots, s);
 }
 
 template <int VAR>

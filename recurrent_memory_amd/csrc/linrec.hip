@@ -578,11 +578,9 @@ __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArg
     int page = b;
     bool later = false;
     if (p.slots != nullptr) {
-        page = p.slots[b];
-        if (page < 0 || page >= p.n_pages) return;
         bool earlier;
-        slot_sharers(p.slots, p.B, b, page, &earlier, &later);
-        if (earlier) return;
+        page = slot_of_row(p.slots, p.B, b, &earlier, &later);
+        if (page < 0 || page >= p.n_pages || earlier) return;
     }
     if (c >= p.D) return;
     float* hp = p.h + static_cast<int64_t>(page) * p.D + c;

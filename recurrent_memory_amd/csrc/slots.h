@@ -5,32 +5,33 @@
 
 namespace dr {
 
-// Whether a row before b, or one after it, names page `slot` too.  Every wave
-// scans the list by itself, four slots a lane at a time (one load for 256 rows),
-// so that the answer is wave-uniform without a barrier.
-__device__ __forceinline__ void slot_sharers(const int* __restrict__ slots, int B, int b, int slot,
-                                             bool* earlier, bool* later) {
+// Row b's page, and whether a row before b, or one after it, names that page too.
+// Every wave scans the list by itself, 256 entries at a time, so that the answer is
+// wave-uniform without a barrier.  The first 256 are loaded along with the row's own
+// entry, before either is looked at, so that a batch of up to 256 rows waits once.
+__device__ __forceinline__ int slot_of_row(const int* __restrict__ slots, int B, int b, bool* earlier,
+                                           bool* later) {
     const int lane = threadIdx.x & 63;
-    bool e = false, l = false;
-    for (int i0 = 0; i0 < B; i0 += 256) {
-        const int i = i0 + 4 * lane;
-        int s[4] = {-1, -1, -1, -1};
-        if (i + 3 < B) {
-            const int4 v = *reinterpret_cast<const int4*>(slots + i);
-            s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-        } else {
+    int s[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (i + j < B) s[j] = slots[i + j];
-        }
+    for (int j = 0; j < 4; ++j) s[j] = slots[min(64 * j + lane, B - 1)];
+    const int slot = slots[b];
+    bool e = false, l = false;
+    for (int i0 = 0;;) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            e |= s[j] == slot && i + j < b;
-            l |= s[j] == slot && i + j > b;
+            const int i = i0 + 64 * j + lane;      // beyond the list: entry B - 1 again, not counted
+            e |= s[j] == slot && i < b;
+            l |= s[j] == slot && i > b && i < B;
         }
+        i0 += 256;
+        if (i0 >= B) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = slots[min(i0 + 64 * j + lane, B - 1)];
     }
     *earlier = __ballot(e) != 0;
     *later = __ballot(l) != 0;
+    return slot;
 }
 
 // The first row after b that names page `slot`, or B.

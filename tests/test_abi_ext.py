@@ -100,7 +100,7 @@ def test_linrec_alignment_and_aliasing():
     assert fwd(ld(), x=FAKE[0] + 8) == DR_E_ALIGN
     assert fwd(ld(), states=FAKE[6] + 4) == DR_E_ALIGN
     assert bwd(ld(), dh0=FAKE[9] + 4) == DR_E_ALIGN
-    assert step(ld(T=1), slots=FAKE[4] + 4) == DR_E_ALIGN
+    assert step(ld(T=1), slots=FAKE[4] + 2) == DR_E_ALIGN          # lists of int32: 4 bytes
     for name in ("x", "g", "beta", "h0"):
         i = ("x", "g", "beta", "h0").index(name)
         assert fwd(ld(), o=FAKE[i]) == DR_E_ALIAS, name
@@ -172,14 +172,15 @@ def test_pages():
     assert copy(pd(), src_pool=FAKE[5], src_pages=0) == DR_E_SHAPE
     assert copy(pd(), src_pool=FAKE[0] + 4096) == DR_E_ALIAS  # a shifted view of the pool
     assert copy(pd(), dst=FAKE[0]) == DR_E_ALIAS
-    assert copy(pd(), src=FAKE[2] + 4) == DR_E_ALIGN
+    assert copy(pd(), src=FAKE[2] + 2) == copy(pd(), pool=FAKE[0] + 4, src_pool=FAKE[5]) == DR_E_ALIGN
     assert compact(pd(), out=FAKE[1]) == DR_E_ALIAS           # slots are read while slots_out is written
     assert compact(pd(), n_live=FAKE[2]) == DR_E_ALIAS
-    assert compact(pd(), n_live=FAKE[3] + 4) == DR_E_ALIGN
+    assert compact(pd(), n_live=FAKE[3] + 2) == DR_E_ALIGN
     assert copy(pd(n=0), dst=None, src=None) == DR_OK         # nothing to do
     if not GPU:
         assert copy(pd()) == copy(pd(), src_pool=FAKE[5], src_pages=3) == DR_E_DEVICE
         assert compact(pd(n=0), slots=None, out=None) == DR_E_DEVICE
+        assert copy(pd(), dst=FAKE[1] + 4) == compact(pd(), slots=FAKE[1] + 4) == DR_E_DEVICE   # part of a list
 
 
 def test_binding_refuses_cpu_tensors():

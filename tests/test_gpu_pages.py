@@ -106,6 +106,38 @@ def test_copy_between_pools_and_repeats():
     assert torch.equal(p4[2], s4[1])
 
 
+def test_lists_that_are_parts_of_longer_ones():
+    """Lists may start at any int32."""
+    announce("pages_list_parts")
+    _, pool = _pool(9, 20, 6)
+    want = _copy_ref(pool, [3, 4], [1, 0])
+    ops.pages_copy(pool, _ints([9, 3, 4])[1:], _ints([7, 7, 7, 1, 0])[3:])
+    out, n_live = ops.pages_compact(pool, _ints([5, 8, 0])[1:])
+    h = pool.clone()
+    x = torch.randn(2, 20, device="cuda")
+    ops.linrec_step(x, torch.zeros_like(x), h, slots=_ints([0, 0, 6, 2])[2:])
+    torch.cuda.synchronize()
+    assert out.tolist() == [1, 0] and n_live.item() == 2
+    assert torch.equal(pool[2:], want[2:]) and torch.equal(pool[0], want[0]) and torch.equal(pool[1], want[8])
+    assert torch.equal(h[6], pool[6] + x[0]) and torch.equal(h[2], pool[2] + x[1])
+
+
+def test_decode_slots_streams_large_pools():
+    """From 128 MiB of states on the accesses are non-temporal: the same bits."""
+    announce("decode_slots_large")
+    for variant in ("gdn", "kda"):
+        B, H = 130, 16
+        t = _step_inputs(variant, "bf16", B, H, 128, 128, seed=9)
+        pool = 0.02 * torch.randn(140, H, 128, 128, device="cuda")
+        slots = torch.randperm(140, generator=torch.Generator().manual_seed(3))[:B].to(torch.int32).cuda()
+        S, want = pool[slots.long()].contiguous(), pool.clone()
+        o = ops.delta_decode_slots(variant, t["q"], t["k"], t["v"], t["beta"], pool, slots, g=t["g"])
+        ow = ops.delta_decode(variant, t["q"], t["k"], t["v"], t["beta"], S, g=t["g"])
+        want[slots.long()] = S
+        torch.cuda.synchronize()
+        assert torch.equal(o, ow) and torch.equal(pool, want)
+
+
 def test_copy_keeps_bit_patterns():
     """Copies move NaN payloads, infinities and subnormals as they are."""
     announce("pages_copy_bits")
