@@ -99,7 +99,7 @@ dr_status delta_linrec_bwd(const dr_linrec_desc* desc, const void* x, const void
  * Sequences name their pages by slot numbers: lists of int32 in device memory,
  * which need be aligned to 4 bytes only.
  */
-#define DR_MAX_PAGES 65536
+#define DR_MAX_PAGES 65536   /* pages of a pool, and entries of a list of slots */
 
 /*
  * delta_linrec_step — one token per sequence.

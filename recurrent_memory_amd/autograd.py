@@ -10,6 +10,11 @@ states itself, so nothing but the inputs is saved.
 ``linear_recurrence(x, g, beta=None, h0=None)`` does the same for the gated linear
 recurrence (``ops.linrec_fwd``, ``ops.linrec_bwd``); it saves the inputs and the
 fp32 state before every 16th token.
+
+To capture a training step in a HIP graph, take its gradients with
+``torch.autograd.grad`` inside the capture, after the eager graphs of the same leaves
+are gone: torch's accumulation of ``.grad`` belongs to the stream that first used the
+leaf, and may not join a capture on another.
 """
 from __future__ import annotations
 

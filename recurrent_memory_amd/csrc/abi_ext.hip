@@ -169,7 +169,9 @@ dr_status delta_linrec_step(const dr_linrec_desc* desc, const void* x, const voi
         dr_status st = check_linrec_desc(desc, true, &sz);
         if (st != DR_OK) return st;
         if (x == nullptr || g == nullptr || h == nullptr || o == nullptr) return DR_E_NULLPTR;
-        if (n_pages < 1 || (slots == nullptr ? n_pages != desc->B : n_pages > DR_MAX_PAGES)) return DR_E_SHAPE;
+        if (n_pages < 1) return DR_E_SHAPE;
+        if (slots == nullptr ? n_pages != desc->B : n_pages > DR_MAX_PAGES || desc->B > DR_MAX_PAGES)
+            return DR_E_SHAPE;
         const void* ptrs[] = {x, g, beta, h, o};
         for (const void* p : ptrs)
             if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;
@@ -202,7 +204,7 @@ dr_status delta_decode_slots(const dr_desc* desc, const void* q, const void* k, 
             return DR_E_NULLPTR;
         st = check_gate_ptrs(desc, beta, wgate, g);
         if (st != DR_OK) return st;
-        if (n_pages < 1 || n_pages > DR_MAX_PAGES) return DR_E_SHAPE;
+        if (n_pages < 1 || n_pages > DR_MAX_PAGES || desc->B > DR_MAX_PAGES) return DR_E_SHAPE;
         const void* ptrs[] = {q, k, v, beta, wgate, g, pool, o};
         for (const void* p : ptrs)
             if (p != nullptr && !aligned16(p)) return DR_E_ALIGN;

@@ -569,12 +569,36 @@ __global__ __launch_bounds__(256) void linrec_clear_kernel(uint4* ws, int64_t n)
         ws[i] = ones;
 }
 
-// One token per sequence.  A workgroup takes 256 * V channels of one row; rows
-// that share a page are all taken by the first of them, in order.
+// V consecutive channels from element i on: one access of 8 or 16 bytes for V = 4.
+template <typename E, int V>
+__device__ __forceinline__ void load_channels(const void* base, int64_t i, float* f) {
+    if constexpr (V == 4) {
+        const float4 v = load4<E>(base, i);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+        f[0] = load_elem<E>(base, i);
+    }
+}
+template <typename E, int V>
+__device__ __forceinline__ void store_channels(void* base, int64_t i, const float* f) {
+    if constexpr (V == 1) {
+        store_elem<E>(base, i, f[0]);
+    } else if constexpr (E::bytes == 4) {
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) = make_uint2(Bf16Even::pack(f), Bf16Even::pack(f + 2));
+    }
+}
+
+// One token per sequence: 8 bytes of state and 3 or 4 values per channel, HBM-bound for
+// large batches, launch-bound for small ones (256 rows of 2048 channels bf16: 3.6 us).
+// A workgroup takes 256 * V channels of one row; rows that share a page are all taken by
+// the first of them, in order.
 template <typename E, bool BETA, int V>
 __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArgs p, int per_row) {
     int b = blockIdx.x / per_row;
     const int c = ((blockIdx.x % per_row) * kStepThreads + threadIdx.x) * V;
+    const bool on = c < p.D;      // lanes behind the row only help to scan the list
     int page = b;
     bool later = false;
     if (p.slots != nullptr) {
@@ -582,26 +606,26 @@ __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArg
         page = slot_of_row(p.slots, p.B, b, &earlier, &later);
         if (page < 0 || page >= p.n_pages || earlier) return;
     }
-    if (c >= p.D) return;
-    float* hp = p.h + static_cast<int64_t>(page) * p.D + c;
+    const int64_t state = static_cast<int64_t>(page) * p.D + c;
     float h[V];
+    if (on) load_channels<F32, V>(p.h, state, h);
+    do {
+        if (on) {
+            const int64_t at = static_cast<int64_t>(b) * p.D + c;
+            float u[V], a[V], w[V];
+            load_channels<E, V>(p.x, at, u);
+            load_channels<E, V>(p.g, at, a);
+            if constexpr (BETA) load_channels<E, V>(p.beta, at, w);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = hp[v];
-    while (true) {
-        const int64_t at = static_cast<int64_t>(b) * p.D + c;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float u = load_elem<E>(p.x, at + v);
-            if constexpr (BETA) u *= load_elem<E>(p.beta, at + v);
-            h[v] = fmaf(__expf(load_elem<E>(p.g, at + v)), h[v], u);
-            store_elem<E>(p.o, at + v, h[v]);
+            for (int v = 0; v < V; ++v) {
+                if constexpr (BETA) u[v] *= w[v];
+                h[v] = fmaf(__expf(a[v]), h[v], u[v]);
+            }
+            store_channels<E, V>(p.o, at, h);
         }
-        if (!later) break;
-        b = next_sharer(p.slots, p.B, b, page);
-        if (b == p.B) break;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) hp[v] = h[v];
+        if (later) b = next_sharer(p.slots, p.B, b, page);
+    } while (later && b < p.B);
+    if (on) store_channels<F32, V>(p.h, state, h);
 }
 
 // ---- plans ----

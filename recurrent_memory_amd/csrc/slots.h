@@ -7,7 +7,7 @@ namespace dr {
 
 // Row b's page, and whether a row before b, or one after it, names that page too.
 // Every wave scans the list by itself, 256 entries at a time, so that the answer is
-// wave-uniform without a barrier.  The first 256 are loaded along with the row's own
+// wave-uniform without a barrier.  Called by whole waves.  The first 256 are loaded along with the row's own
 // entry, before either is looked at, so that a batch of up to 256 rows waits once.
 __device__ __forceinline__ int slot_of_row(const int* __restrict__ slots, int B, int b, bool* earlier,
                                            bool* later) {
@@ -34,11 +34,14 @@ __device__ __forceinline__ int slot_of_row(const int* __restrict__ slots, int B,
     return slot;
 }
 
-// The first row after b that names page `slot`, or B.
+// The first row after b that names page `slot`, or B.  Called by whole waves.
 __device__ __forceinline__ int next_sharer(const int* __restrict__ slots, int B, int b, int slot) {
-    for (++b; b < B; ++b)
-        if (slots[b] == slot) break;
-    return b;
+    const int lane = threadIdx.x & 63;
+    for (int i0 = b + 1; i0 < B; i0 += 64) {
+        const uint64_t found = __ballot(i0 + lane < B && slots[min(i0 + lane, B - 1)] == slot);
+        if (found != 0) return i0 + __ffsll(static_cast<unsigned long long>(found)) - 1;
+    }
+    return B;
 }
 
 }  // namespace dr

@@ -142,18 +142,21 @@ def test_step_and_slots():
     assert step(ld(T=1), n=0) == DR_E_SHAPE
     assert step(ld(T=1), n=ops.MAX_PAGES + 1) == DR_E_SHAPE
     assert step(ld(T=1), slots=None, n=3) == DR_E_SHAPE       # without slots the pool is the batch
+    assert step(ld(T=1, B=ops.MAX_PAGES + 1, D=4)) == DR_E_SHAPE
     d = ops.DrDesc(B=2, T=1, H=3, d_k=128, d_v=128, chunk=64, variant=1, dtype=1)
     assert dec(None) == DR_E_NULLPTR
     for name in ("q", "k", "v", "beta", "g", "pool", "slots", "o"):
         assert dec(d, **{name: None}) == DR_E_NULLPTR, name
     assert dec(d, wgate=FAKE[9]) == DR_E_UNSUPPORTED
     assert dec(d, n=0) == dec(d, n=ops.MAX_PAGES + 1) == DR_E_SHAPE
+    assert dec(ops.DrDesc(B=ops.MAX_PAGES + 1, T=1, H=1, d_k=64, d_v=64, chunk=64, variant=1, dtype=1)) == DR_E_SHAPE
     assert dec(d, pool=FAKE[6] + 8) == DR_E_ALIGN
     assert dec(d, o=FAKE[6] + 15 * 3 * 128 * 128 * 4) == DR_E_ALIAS       # over the pool's last page
     assert dec(d, pool=FAKE[7]) == DR_E_ALIAS                             # over the slots
     assert dec(ops.DrDesc(B=2, T=2, H=3, d_k=128, d_v=128, chunk=64, variant=1, dtype=1)) == DR_E_SHAPE
     if not GPU:
         assert step(ld(T=1), slots=None, n=2) == DR_E_DEVICE
+        assert step(ld(T=1, B=ops.MAX_PAGES + 1, D=4), slots=None, n=ops.MAX_PAGES + 1) == DR_E_DEVICE
         assert step(ld(T=1)) == dec(d) == DR_E_DEVICE
 
 

@@ -50,7 +50,7 @@ def test_forward_and_backward(dtype, B, T, D):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("B,T,D,scale", [(1, 20000, 70, 1 / 512), (2, 9000, 256, 1 / 64), (1, 33000, 33, 1 / 16)])
+@pytest.mark.parametrize("B,T,D,scale", [(1, 20000, 70, 1 / 512), (2, 9000, 256, 1 / 64), (2, 2200, 33, 1 / 16)])
 def test_long_sequences(dtype, B, T, D, scale):
     """Slow decays over many tiles: what is carried across them matters."""
     announce("linrec_long", dtype, B, T, D, scale)
@@ -259,6 +259,37 @@ def test_autograd(dtype, with_beta, with_h0):
     assert not o.requires_grad
 
 
+def test_training_step_in_a_graph():
+    """Forward and torch.autograd.grad captured together and replayed on new inputs."""
+    announce("linrec_autograd_graph")
+    x, g, b, s, dO, dhT = R.inputs(2, 300, 66, torch.float32, True, True, 0.2, seed=21)
+    leaves = [t.requires_grad_(True) for t in (x, g, b, s)]
+
+    def train():
+        o, hT = linear_recurrence(x, g, b, s)
+        return torch.autograd.grad((o, hT), leaves, (dO, dhT))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        train()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    gph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gph):
+        grads = train()
+    for rep in range(3):
+        new = R.inputs(2, 300, 66, torch.float32, True, True, 0.2, seed=200 + rep)
+        with torch.no_grad():
+            for a, c in zip((x, g, b, s, dO, dhT), new):
+                a.copy_(c)
+        gph.replay()
+        torch.cuda.synchronize()
+        ref = R.grads_and_bounds(*new)
+        for n, got in zip(("dx", "dg", "dbeta", "dh0"), grads):
+            R.check(n, got, *ref[n])
+
+
 def test_more_than_2_to_the_31_elements():
     """Offsets past 32 bits: the last tokens of two sequences of 2^30 + elements each,
     whose states follow from the last reset."""
@@ -328,6 +359,22 @@ def test_step(dtype, B, N, D, slots):
         assert torch.equal(got.t[untouched], pool[untouched])
         got.check("pool")
         out.check("o", full=False)
+
+
+def test_step_with_many_rows_on_a_page():
+    """Lists longer than one scan; pages shared by rows far apart and by runs of rows."""
+    announce("linrec_step_shared")
+    B, N, D = 700, 500, 9
+    slots = [i % 450 for i in range(B)]
+    slots[100:140], slots[-1], slots[5] = [499] * 40, 499, -3
+    x, g, b, _, _, _ = R.inputs(B, 1, D, torch.float32, True, False, seed=31)
+    x, g, b = x[:, 0], g[:, 0], b[:, 0]
+    pool = torch.randn(N, D, generator=torch.Generator().manual_seed(4)).cuda()
+    h, err, o, oerr = _step_ref(x, g, b, pool, slots)
+    out = ops.linrec_step(x, g, pool, beta=b, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    R.check("h", pool, h, err)
+    rows = sorted(o)
+    R.check("o", out[rows], torch.stack([o[r] for r in rows]), torch.stack([oerr[r] for r in rows]))
 
 
 def test_step_follows_the_sequence_form():
