@@ -36,7 +36,7 @@ int dr_ext_version(void);
  * is the delta rule's decay and write without the read that makes a matrix
  * memory error-correcting.  g = -inf forgets everything before its token (a
  * document's border in a packed sequence); there is no floor.  g > 0 is not
- * refused, but the decays of 256 consecutive tokens are multiplied up, and
+ * refused, but the decays of up to 384 consecutive tokens are multiplied up, and
  * their product must stay inside fp32.  Tokens with g = 0 and x = 0 leave the
  * state as it is (the padding of a short sequence in a batch).
  *

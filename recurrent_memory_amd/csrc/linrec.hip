@@ -35,18 +35,20 @@ namespace dr {
 namespace {
 
 constexpr int kTok = 16;            // tokens of a wave, and tokens per row of `states`
-constexpr int kMaxWaves = 8;        // waves of a workgroup: tiles of up to 128 tokens
+constexpr int kMaxWaves = 8;        // waves of a workgroup: tiles of 128 tokens
+constexpr int kSingleWaves = 16;    // sequences of up to 256 tokens are one tile
 constexpr int kGroup = 16;          // tiles from one published state to the next
 constexpr int kCarryWave = kMaxWaves - 1;   // the last wave collects the state, the others maps,
 constexpr int kPer = (kGroup - 1 + kMaxWaves - 2) / (kMaxWaves - 1);   // this many each
 constexpr int kStepThreads = 256;
 constexpr uint32_t kMaxGrid = 1u << 20;
 
-// Memory accesses of the tiles.  NT: non-temporal, where waves cover whole cache lines
-// and every line passes once (B=1 T=32768 D=2048 bf16: forward 109 us plain, 102 us
-// non-temporal; backward 185 and 170 us); plain where two columns share lines, which
-// then meet in a cache (B=3 T=8000 D=1000 bf16: forward 55 us plain, 59 us non-temporal;
-// backward 99 and 118 us).
+// Memory accesses of the tiles.  NT: non-temporal, where rows are whole cache lines and
+// every line passes once (B=1 T=32768 D=2048 bf16: forward 109 us plain, 102 us
+// non-temporal, backward 185 and 170 us; D=2112, where a wave's end falls inside a row,
+// B=4 T=4096: forward 66 and 60 us, backward 110 and 101 us); plain where two waves share
+// lines, which then meet in a cache (B=3 T=8000 D=1000 bf16: forward 55 us plain, 59 us
+// non-temporal; backward 99 and 118 us).
 template <bool NT, typename P>
 __device__ __forceinline__ P load_word(const P* p) {
     if constexpr (NT) return __builtin_nontemporal_load(p);
@@ -193,7 +195,7 @@ __device__ __forceinline__ void collect_state(const uint32_t* at, int nch, float
 // What a tile's waves share.
 template <int VEC>
 struct Joint {
-    float2 wave[kMaxWaves][64 * VEC];     // the waves' maps, in the order they act
+    float2 wave[kSingleWaves][64 * VEC];  // the waves' maps, in the order they act
     float2 tile[kMaxWaves - 1][64 * VEC]; // maps of the tiles before this one, of its group
     float carry[64 * VEC];                // the state in front of those
     uint32_t ticket;
@@ -333,7 +335,7 @@ struct Place {
 
 // The words of n (0 .. 16) tokens from element `row` on, rows of D elements; zeros
 // beyond them and in lanes without channels (g = 0, x = 0, dO = 0 act as identity).
-template <typename W, bool UNI>
+template <bool NT, typename W, bool UNI>
 __device__ __forceinline__ void load_tokens(const void* base, int64_t row, const Place<W, UNI>& at, int D,
                                             int n, uint32_t* r) {
     const typename W::T* p = static_cast<const typename W::T*>(base) + row;
@@ -344,15 +346,15 @@ __device__ __forceinline__ void load_tokens(const void* base, int64_t row, const
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
             const typename W::T* q = p + static_cast<int64_t>(i) * D + at.c;
-            if (i < n) r[i] = at.lone ? static_cast<uint32_t>(*q) : W::template load<UNI>(q);
+            if (i < n) r[i] = at.lone ? static_cast<uint32_t>(*q) : W::template load<NT>(q);
         }
     } else if (n == kTok) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) r[i] = W::template load<UNI>(p + static_cast<int64_t>(i) * D + at.c);
+        for (int i = 0; i < kTok; ++i) r[i] = W::template load<NT>(p + static_cast<int64_t>(i) * D + at.c);
     } else {
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
-            if (i < n) r[i] = W::template load<UNI>(p + static_cast<int64_t>(i) * D + at.c);
+            if (i < n) r[i] = W::template load<NT>(p + static_cast<int64_t>(i) * D + at.c);
     }
 }
 
@@ -364,8 +366,8 @@ __device__ __forceinline__ void forget_derived(uint32_t* r) {
     for (int i = 0; i < kTok; ++i) asm volatile("" : "+v"(r[i]));
 }
 
-template <typename W, bool BETA, bool UNI>
-__global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_fwd_kernel(LinrecArgs p, Tiles ts) {
+template <typename W, bool BETA, bool UNI, bool NT>
+__global__ __launch_bounds__(kSingleWaves * 64) void linrec_fwd_kernel(LinrecArgs p, Tiles ts) {
     constexpr int VEC = W::VEC;
     __shared__ Joint<VEC> J;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -380,9 +382,9 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_fwd_kernel(LinrecArg
         const int n = static_cast<int>(p.T - t0 >= kTok ? kTok : p.T > t0 ? p.T - t0 : 0);
         const int64_t row = (at.seq * p.T + t0) * p.D;
         uint32_t xr[kTok], gr[kTok], br[kTok];
-        load_tokens(p.x, row, at, p.D, n, xr);
-        load_tokens(p.g, row, at, p.D, n, gr);
-        if constexpr (BETA) load_tokens(p.beta, row, at, p.D, n, br);
+        load_tokens<NT>(p.x, row, at, p.D, n, xr);
+        load_tokens<NT>(p.g, row, at, p.D, n, gr);
+        if constexpr (BETA) load_tokens<NT>(p.beta, row, at, p.D, n, br);
 
         // one token's decay and written value
         auto token = [&](int i, float* a, float* u) {
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_fwd_kernel(LinrecArg
             token(i, a, u);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[v], h[v], u[v]);
-            if (i < n) W::template store<UNI>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+            if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
         }
         // beyond the last token h is carried along unchanged
         if (p.hT != nullptr && t0 + n == p.T) {
@@ -438,8 +440,8 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_fwd_kernel(LinrecArg
     }
 }
 
-template <typename W, bool BETA, bool UNI>
-__global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_bwd_kernel(LinrecBwdArgs p, Tiles ts) {
+template <typename W, bool BETA, bool UNI, bool NT>
+__global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwdArgs p, Tiles ts) {
     constexpr int VEC = W::VEC;
     __shared__ Joint<VEC> J;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -454,10 +456,10 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_bwd_kernel(LinrecBwd
         const int n = static_cast<int>(p.T - t0 >= kTok ? kTok : p.T > t0 ? p.T - t0 : 0);
         const int64_t row = (at.seq * p.T + t0) * p.D;
         uint32_t xr[kTok], gr[kTok], br[kTok], dr[kTok];
-        load_tokens(p.g, row, at, p.D, n, gr);
-        load_tokens(p.dO, row, at, p.D, n, dr);
-        load_tokens(p.x, row, at, p.D, n, xr);
-        if constexpr (BETA) load_tokens(p.beta, row, at, p.D, n, br);
+        load_tokens<NT>(p.g, row, at, p.D, n, gr);
+        load_tokens<NT>(p.dO, row, at, p.D, n, dr);
+        load_tokens<NT>(p.x, row, at, p.D, n, xr);
+        if constexpr (BETA) load_tokens<NT>(p.beta, row, at, p.D, n, br);
         float h[VEC];
         const bool here = at.nch > 0 && n > 0;
         {
@@ -548,9 +550,9 @@ __global__ __launch_bounds__(kMaxWaves * 64, 4) void linrec_bwd_kernel(LinrecBwd
                 }
                 if (i < n) {
                     const int64_t el = row + static_cast<int64_t>(i) * p.D;
-                    W::template store<UNI>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
-                    W::template store<UNI>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
-                    if constexpr (BETA) W::template store<UNI>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
+                    W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
+                    W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
+                    if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
                 }
             }
         }
@@ -630,7 +632,12 @@ __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArg
 
 // ---- plans ----
 
-int64_t chain_of(int T) { return (static_cast<int64_t>(T) + kMaxWaves * kTok - 1) / (kMaxWaves * kTok); }
+// Tiles of a sequence.  One tile needs no counter, no maps and no clearing of them
+// (B=32 T=200 D=2048 bf16: forward 25 us as two tiles, 23 us as one; backward 43 and 37).
+int64_t chain_of(int T) {
+    if (T <= kSingleWaves * kTok) return 1;
+    return (static_cast<int64_t>(T) + kMaxWaves * kTok - 1) / (kMaxWaves * kTok);
+}
 
 // Workspace: the counters, the maps, the states; none if a tile covers T.
 size_t counter_bytes(size_t channels) { return round_up_256((channels + 63) / 64 * kCounter * 4); }
@@ -658,22 +665,19 @@ Tiles plan(int B, int T, int D, int vec, void* ws) {
     return t;
 }
 
-// Waves of a workgroup: what T needs, all as soon as there is more than one tile.
-int waves_of(int T) {
-    const int64_t w = (static_cast<int64_t>(T) + kTok - 1) / kTok;
-    return w < kMaxWaves ? static_cast<int>(w) : kMaxWaves;
-}
+// Waves of a workgroup: what T needs if one tile covers it.
+int waves_of(int T) { return chain_of(T) > 1 ? kMaxWaves : (T + kTok - 1) / kTok; }
 
 struct FwdLaunch {
-    template <typename W, bool BETA, bool UNI>
+    template <typename W, bool BETA, bool UNI, bool NT>
     static void go(const LinrecArgs& a, const Tiles& t, dim3 grid, dim3 block, hipStream_t s) {
-        hipLaunchKernelGGL((linrec_fwd_kernel<W, BETA, UNI>), grid, block, 0, s, a, t);
+        hipLaunchKernelGGL((linrec_fwd_kernel<W, BETA, UNI, NT>), grid, block, 0, s, a, t);
     }
 };
 struct BwdLaunch {
-    template <typename W, bool BETA, bool UNI>
+    template <typename W, bool BETA, bool UNI, bool NT>
     static void go(const LinrecBwdArgs& a, const Tiles& t, dim3 grid, dim3 block, hipStream_t s) {
-        hipLaunchKernelGGL((linrec_bwd_kernel<W, BETA, UNI>), grid, block, 0, s, a, t);
+        hipLaunchKernelGGL((linrec_bwd_kernel<W, BETA, UNI, NT>), grid, block, 0, s, a, t);
     }
 };
 
@@ -689,14 +693,19 @@ hipError_t launch_tiles(const Args& a, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     const dim3 grid(t.n < kMaxGrid ? t.n : kMaxGrid), block(static_cast<unsigned>(waves_of(a.T)) * 64);
-    // rows of whole words and whole waves: scalar row addresses (see Place)
+    // Rows of whole words: whole waves of them have scalar row addresses (see Place), whole
+    // cache lines (128 bytes, 32 words) are streamed.
     if constexpr (!W::kOdd) {
         if (t.row_lanes % 64 == 0) {
-            L::template go<W, BETA, true>(a, t, grid, block, s);
+            L::template go<W, BETA, true, true>(a, t, grid, block, s);
+            return hipGetLastError();
+        }
+        if (t.row_lanes % 32 == 0) {
+            L::template go<W, BETA, false, true>(a, t, grid, block, s);
             return hipGetLastError();
         }
     }
-    L::template go<W, BETA, false>(a, t, grid, block, s);
+    L::template go<W, BETA, false, false>(a, t, grid, block, s);
     return hipGetLastError();
 }
 

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 SHAPES = [(1, 1, 1), (2, 1, 7), (3, 2, 64), (1, 15, 3), (2, 16, 130), (2, 17, 65), (1, 31, 128), (3, 33, 63),
           (1, 127, 129), (2, 128, 8), (1, 129, 256), (2, 255, 127), (1, 256, 130), (2, 257, 1), (5, 300, 10),
-          (1, 513, 66), (2, 1000, 101), (1, 4099, 48), (70, 40, 2), (3, 777, 1001), (2, 520, 2048)]
+          (1, 513, 66), (2, 1000, 101), (1, 4099, 48), (70, 40, 2), (3, 777, 1001), (2, 520, 2048), (3, 290, 192)]
 
 
 def _fwd_check(x, g, b, h0, want_states=True):
