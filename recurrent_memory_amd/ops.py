@@ -446,18 +446,19 @@ def ttt_pre(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bet
 # share small: one comparison per property on the way through, the words of a refusal
 # only when one fails.
 
-def _need(name, t, shape, dtype, dev):
-    """_check, written for tensors that pass it."""
-    if t is None or t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        _check(name, t, shape, dtype, dev)
+def _need(name, t, shape, dtype, gpu):
+    """_check on GPU number ``gpu``, written for tensors that pass it."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        _check(name, t, shape, dtype, torch.device("cuda", gpu))
 
 
-def _gpu(name: str, t: torch.Tensor) -> torch.device:
+def _gpu(name: str, t: torch.Tensor) -> int:
+    """The number of the GPU that holds t."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a GPU tensor, got device {t.device}")
-    return t.device
+    return t.get_device()
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -467,25 +468,34 @@ def _dtype_code(t: torch.Tensor) -> int:
     return code
 
 
-def _enqueue(dev: torch.device, stream, fn, *args, fresh=()):
-    """Call ``fn(*args, stream)`` with ``dev`` current, on ``stream`` or else the
-    device's current stream.  ``fresh``: tensors allocated for this call, marked as
-    used on ``stream`` if one is given."""
-    if dev.index != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return _enqueue(dev, stream, fn, *args, fresh=fresh)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        handle = stream.cuda_stream
-        for t in fresh:
-            if t is not None:
-                t.record_stream(stream)
-    st = fn(*args, handle)
+_current_gpu = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _enqueue(gpu: int, fn, *args):
+    """Call ``fn(*args, stream)`` with ``gpu`` current, on its current stream."""
+    if gpu != _current_gpu():
+        with torch.cuda.device(gpu):
+            return _enqueue(gpu, fn, *args)
+    st = fn(*args, _current_stream(gpu))
     if st != 0:
         _raise(st)
+
+
+def _on_stream(stream, name: str, t: torch.Tensor, fn, *args):
+    """``fn(*args)`` with ``stream`` current.  What the call allocates belongs to that
+    stream, so the kernels never write into memory that work queued elsewhere still
+    uses; the results are marked as used on the caller's stream too."""
+    gpu = _gpu(name, t)
+    if stream.device.index != gpu:
+        raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
+    caller = torch.cuda.current_stream(gpu)
+    with torch.cuda.stream(stream):
+        res = fn(*args)
+    for r in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
+        if r is not None:
+            r.record_stream(caller)
+    return res
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -497,31 +507,30 @@ def _linrec_bytes(entry: str, B: int, T: int, D: int, code: int) -> int:
     return workspace_bytes(entry, LinrecDesc(B, T, D, code))
 
 
-def _linrec_workspace(need: int, dev, workspace: Optional[torch.Tensor]):
-    """(address or None, bytes, the tensor if allocated here)."""
+def _linrec_workspace(need: int, gpu: int, workspace: Optional[torch.Tensor]):
+    """(tensor or None, bytes) of a call's workspace, allocated here if not given."""
     if need == 0:
-        return None, 0, None
+        return None, 0
     if workspace is None:
-        fresh = torch.empty(need, dtype=torch.uint8, device=dev)
-        return fresh.data_ptr(), need, fresh
-    if workspace.device != dev or not workspace.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=gpu), need
+    if workspace.get_device() != gpu or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the call's device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _linrec_check(x, g, beta, dims: int):
-    """(device, shape, dtype, its code) of the inputs."""
-    dev = _gpu("x", x)
+    """(GPU, shape, dtype, its code) of the inputs."""
+    gpu = _gpu("x", x)
     shape, dt = x.shape, x.dtype
     if len(shape) != dims:
         raise ValueError(f"x: expected {dims} dimensions, got shape {tuple(shape)}")
     code = _dtype_code(x)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _need("g", g, shape, dt, dev)
+    _need("g", g, shape, dt, gpu)
     if beta is not None:
-        _need("beta", beta, shape, dt, dev)
-    return dev, shape, dt, code
+        _need("beta", beta, shape, dt, gpu)
+    return gpu, shape, dt, code
 
 
 def linrec_fwd(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = None,
@@ -537,27 +546,29 @@ def linrec_fwd(x: torch.Tensor, g: torch.Tensor, beta: Optional[torch.Tensor] = 
     wanted or given; ``h_T=h0`` updates in place) and the states that ``linrec_bwd``
     needs (None unless wanted or given), [B, ceil(T / LINREC_BLOCK), D] fp32.
     """
+    if stream is not None:
+        return _on_stream(stream, "x", x, linrec_fwd, x, g, beta, h0, o, h_T, want_state, states, want_states, None,
+                          workspace)
     lib = load_library()
-    dev, shape, dt, code = _linrec_check(x, g, beta, 3)
+    gpu, shape, dt, code = _linrec_check(x, g, beta, 3)
     B, T, D = shape
     if h0 is not None:
-        _need("h0", h0, (B, D), torch.float32, dev)
-    new_o = new_h = new_s = None
+        _need("h0", h0, (B, D), torch.float32, gpu)
     if o is None:
-        o = new_o = torch.empty_like(x)
+        o = torch.empty_like(x)
     else:
-        _need("o", o, shape, dt, dev)
+        _need("o", o, shape, dt, gpu)
     if h_T is not None:
-        _need("h_T", h_T, (B, D), torch.float32, dev)
+        _need("h_T", h_T, (B, D), torch.float32, gpu)
     elif want_state:
-        h_T = new_h = torch.empty((B, D), dtype=torch.float32, device=dev)
+        h_T = torch.empty((B, D), dtype=torch.float32, device=gpu)
     if states is not None:
-        _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
+        _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, gpu)
     elif want_states:
-        states = new_s = torch.empty((B, -(-T // LINREC_BLOCK), D), dtype=torch.float32, device=dev)
-    ws, wn, keep = _linrec_workspace(_linrec_bytes("linrec_fwd", B, T, D, code), dev, workspace)
-    _enqueue(dev, stream, lib.delta_linrec_fwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
-             _addr(h0), o.data_ptr(), _addr(h_T), _addr(states), ws, wn, fresh=(new_o, new_h, new_s, keep))
+        states = torch.empty((B, -(-T // LINREC_BLOCK), D), dtype=torch.float32, device=gpu)
+    ws, wn = _linrec_workspace(_linrec_bytes("linrec_fwd", B, T, D, code), gpu, workspace)
+    _enqueue(gpu, lib.delta_linrec_fwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+             _addr(h0), o.data_ptr(), _addr(h_T), _addr(states), _addr(ws), wn)
     return o, h_T, states
 
 
@@ -571,35 +582,34 @@ def linrec_bwd(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, dO: torch
     """Gradients of ``linrec_fwd``: dict of dx, dg, dbeta (None without beta) in x's
     dtype and dh0 (fp32, None unless wanted).  ``states`` as ``linrec_fwd`` returned it
     for these inputs.  ``out`` may supply any of these tensors."""
+    if stream is not None:
+        return _on_stream(stream, "x", x, linrec_bwd, x, g, states, dO, beta, dh_T, want_dh0, None, workspace, out)
     lib = load_library()
-    dev, shape, dt, code = _linrec_check(x, g, beta, 3)
+    gpu, shape, dt, code = _linrec_check(x, g, beta, 3)
     B, T, D = shape
-    _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, dev)
-    _need("dO", dO, shape, dt, dev)
+    _need("states", states, (B, -(-T // LINREC_BLOCK), D), torch.float32, gpu)
+    _need("dO", dO, shape, dt, gpu)
     if dh_T is not None:
-        _need("dh_T", dh_T, (B, D), torch.float32, dev)
+        _need("dh_T", dh_T, (B, D), torch.float32, gpu)
     given = out or {}
     for name in given:
         if name not in _LINREC_GRADS or (name == "dbeta" and beta is None):
             raise ValueError(f"{name} is not an output of this call")
-    res, fresh = {}, []
+    res = {}
     for name in _LINREC_GRADS:
         t = given.get(name)
         if t is not None:
-            _need(name, t, (B, D) if name == "dh0" else shape, torch.float32 if name == "dh0" else dt, dev)
+            _need(name, t, (B, D) if name == "dh0" else shape, torch.float32 if name == "dh0" else dt, gpu)
         elif name == "dh0":
             if want_dh0:
-                t = torch.empty((B, D), dtype=torch.float32, device=dev)
-                fresh.append(t)
+                t = torch.empty((B, D), dtype=torch.float32, device=gpu)
         elif name != "dbeta" or beta is not None:
             t = torch.empty_like(x)
-            fresh.append(t)
         res[name] = t
-    ws, wn, keep = _linrec_workspace(_linrec_bytes("linrec_bwd", B, T, D, code), dev, workspace)
-    fresh.append(keep)
-    _enqueue(dev, stream, lib.delta_linrec_bwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+    ws, wn = _linrec_workspace(_linrec_bytes("linrec_bwd", B, T, D, code), gpu, workspace)
+    _enqueue(gpu, lib.delta_linrec_bwd, LinrecDesc(B, T, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
              states.data_ptr(), dO.data_ptr(), _addr(dh_T), res["dx"].data_ptr(), res["dg"].data_ptr(),
-             _addr(res["dbeta"]), _addr(res["dh0"]), ws, wn, fresh=fresh)
+             _addr(res["dbeta"]), _addr(res["dh0"]), _addr(ws), wn)
     return res
 
 
@@ -611,23 +621,23 @@ def linrec_step(x: torch.Tensor, g: torch.Tensor, h: torch.Tensor, beta: Optiona
     [n_pages, D] of which row b's state is page slots[b]; rows with a slot outside the
     pool are skipped (their rows of ``o`` are not written), rows that share a page act
     in order."""
+    if stream is not None:
+        return _on_stream(stream, "x", x, linrec_step, x, g, h, beta, slots, o)
     lib = load_library()
-    dev, shape, dt, code = _linrec_check(x, g, beta, 2)
+    gpu, shape, dt, code = _linrec_check(x, g, beta, 2)
     B, D = shape
     if h.dim() != 2:
         raise ValueError(f"h: expected 2 dimensions, got shape {tuple(h.shape)}")
     pages = h.shape[0]
-    _need("h", h, (B if slots is None else pages, D), torch.float32, dev)
+    _need("h", h, (B if slots is None else pages, D), torch.float32, gpu)
     if slots is not None:
-        _need("slots", slots, (B,), torch.int32, dev)
-    fresh = ()
+        _need("slots", slots, (B,), torch.int32, gpu)
     if o is None:
         o = torch.empty_like(x)
-        fresh = (o,)
     else:
-        _need("o", o, shape, dt, dev)
-    _enqueue(dev, stream, lib.delta_linrec_step, LinrecDesc(B, 1, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
-             h.data_ptr(), pages, _addr(slots), o.data_ptr(), fresh=fresh)
+        _need("o", o, shape, dt, gpu)
+    _enqueue(gpu, lib.delta_linrec_step, LinrecDesc(B, 1, D, code), x.data_ptr(), g.data_ptr(), _addr(beta),
+             h.data_ptr(), pages, _addr(slots), o.data_ptr())
     return o
 
 
@@ -638,48 +648,48 @@ def delta_decode_slots(variant: str, q: torch.Tensor, k: torch.Tensor, v: torch.
     """``delta_decode`` on a pool of states [n_pages, H, dv, dk] fp32, updated in place:
     row b's state is page slots[b] ([B] int32).  Rows with a slot outside the pool are
     skipped (their rows of ``o`` are not written); rows that share a page act in order."""
+    if stream is not None:
+        return _on_stream(stream, "q", q, delta_decode_slots, variant, q, k, v, beta, pool, slots, wgate, g, o)
     lib = load_library()
     var = VARIANTS[variant]
-    dev = _gpu("q", q)
+    gpu = _gpu("q", q)
     if q.dim() != 3 or v.dim() != 3 or pool.dim() != 4:
         raise ValueError("expected q [B, H_k, dk], v [B, H, dv] and pool [n_pages, H, dv, dk]")
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
     dt, code = q.dtype, _dtype_code(q)
-    _need("q", q, (B, Hk, dk), dt, dev)
-    _need("k", k, (B, Hk, dk), dt, dev)
-    _need("v", v, (B, H, dv), dt, dev)
-    _need("beta", beta, (B, H, dk) if variant in _CHANNEL_BETA else (B, H), dt, dev)
+    _need("q", q, (B, Hk, dk), dt, gpu)
+    _need("k", k, (B, Hk, dk), dt, gpu)
+    _need("v", v, (B, H, dv), dt, gpu)
+    _need("beta", beta, (B, H, dk) if variant in _CHANNEL_BETA else (B, H), dt, gpu)
     if variant == "gdn2":
-        _need("wgate", wgate, (B, H, dv), dt, dev)
+        _need("wgate", wgate, (B, H, dv), dt, gpu)
     elif wgate is not None:
         raise ValueError("only gdn2 takes a write gate")
     if variant == "deltanet":
         if g is not None:
             raise ValueError("deltanet takes no decay")
     else:
-        _need("g", g, (B, H) if variant == "gdn" else (B, H, dk), dt, dev)
+        _need("g", g, (B, H) if variant == "gdn" else (B, H, dk), dt, gpu)
     pages = pool.shape[0]
-    _need("pool", pool, (pages, H, dv, dk), torch.float32, dev)
-    _need("slots", slots, (B,), torch.int32, dev)
-    fresh = ()
+    _need("pool", pool, (pages, H, dv, dk), torch.float32, gpu)
+    _need("slots", slots, (B,), torch.int32, gpu)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=dt, device=dev)
-        fresh = (o,)
+        o = torch.empty((B, H, dv), dtype=dt, device=gpu)
     else:
-        _need("o", o, (B, H, dv), dt, dev)
-    _enqueue(dev, stream, lib.delta_decode_slots, DrDesc(B, 1, H, dk, dv, 64, var, code, Hk), q.data_ptr(),
+        _need("o", o, (B, H, dv), dt, gpu)
+    _enqueue(gpu, lib.delta_decode_slots, DrDesc(B, 1, H, dk, dv, 64, var, code, Hk), q.data_ptr(),
              k.data_ptr(), v.data_ptr(), beta.data_ptr(), _addr(wgate), _addr(g), pool.data_ptr(), pages,
-             slots.data_ptr(), o.data_ptr(), fresh=fresh)
+             slots.data_ptr(), o.data_ptr())
     return o
 
 
-def _page(name: str, t: torch.Tensor, dev) -> int:
+def _page(name: str, t: torch.Tensor, gpu) -> int:
     """Floats per page of a pool [n_pages, ...]."""
     shape = t.shape
     if len(shape) < 2:
         raise ValueError(f"{name}: expected [n_pages, ...], got shape {tuple(shape)}")
-    _need(name, t, shape, torch.float32, dev)
+    _need(name, t, shape, torch.float32, gpu)
     return t.numel() // shape[0] if shape[0] else 0
 
 
@@ -689,17 +699,19 @@ def pages_copy(pool: torch.Tensor, dst: torch.Tensor, src: torch.Tensor,
     ``pool``) to page dst[i] of ``pool``, src[i] = -1 clears it.  ``pool`` [n_pages, ...]
     fp32, ``dst`` and ``src`` [n] int32.  Entries act in order; one with another number
     outside its pool does nothing.  Returns ``pool``."""
+    if stream is not None:
+        return _on_stream(stream, "pool", pool, pages_copy, pool, dst, src, src_pool)
     lib = load_library()
-    dev = _gpu("pool", pool)
-    page = _page("pool", pool, dev)
+    gpu = _gpu("pool", pool)
+    page = _page("pool", pool, gpu)
     if src_pool is None:
         src_pool = pool
-    elif _page("src_pool", src_pool, dev) != page:
+    elif _page("src_pool", src_pool, gpu) != page:
         raise ValueError(f"src_pool: pages of {tuple(src_pool.shape[1:])}, expected {tuple(pool.shape[1:])}")
     n = dst.numel()
-    _need("dst", dst, (n,), torch.int32, dev)
-    _need("src", src, (n,), torch.int32, dev)
-    _enqueue(dev, stream, lib.delta_pages_copy, PagesDesc(page, pool.shape[0], n), pool.data_ptr(), dst.data_ptr(),
+    _need("dst", dst, (n,), torch.int32, gpu)
+    _need("src", src, (n,), torch.int32, gpu)
+    _enqueue(gpu, lib.delta_pages_copy, PagesDesc(page, pool.shape[0], n), pool.data_ptr(), dst.data_ptr(),
              src_pool.data_ptr(), src_pool.shape[0], src.data_ptr())
     return pool
 
@@ -710,20 +722,21 @@ def pages_compact(pool: torch.Tensor, slots: torch.Tensor, slots_out: Optional[t
     ``slots`` [n] int32 names the live sequences' pages (numbers outside the pool: ended
     sequences).  Returns (slots_out [n] int32, where each page is now, -1 for ended
     sequences; n_live [1] int32)."""
+    if stream is not None:
+        return _on_stream(stream, "pool", pool, pages_compact, pool, slots, slots_out, n_live)
     lib = load_library()
-    dev = _gpu("pool", pool)
-    page = _page("pool", pool, dev)
+    gpu = _gpu("pool", pool)
+    page = _page("pool", pool, gpu)
     n = slots.numel()
-    _need("slots", slots, (n,), torch.int32, dev)
-    new_s = new_n = None
+    _need("slots", slots, (n,), torch.int32, gpu)
     if slots_out is None:
-        slots_out = new_s = torch.empty_like(slots)
+        slots_out = torch.empty_like(slots)
     else:
-        _need("slots_out", slots_out, (n,), torch.int32, dev)
+        _need("slots_out", slots_out, (n,), torch.int32, gpu)
     if n_live is None:
-        n_live = new_n = torch.empty(1, dtype=torch.int32, device=dev)
+        n_live = torch.empty(1, dtype=torch.int32, device=gpu)
     else:
-        _need("n_live", n_live, (1,), torch.int32, dev)
-    _enqueue(dev, stream, lib.delta_pages_compact, PagesDesc(page, pool.shape[0], n), pool.data_ptr(),
-             slots.data_ptr(), slots_out.data_ptr(), n_live.data_ptr(), fresh=(new_s, new_n))
+        _need("n_live", n_live, (1,), torch.int32, gpu)
+    _enqueue(gpu, lib.delta_pages_compact, PagesDesc(page, pool.shape[0], n), pool.data_ptr(), slots.data_ptr(),
+             slots_out.data_ptr(), n_live.data_ptr())
     return slots_out, n_live

@@ -191,19 +191,31 @@ def test_same_results_on_every_run(B, T, D):
 
 
 def test_stream_argument():
+    """Results of a call on another stream, while the caller's stream still works on memory
+    that was freed before the call."""
     announce("linrec_stream")
     x, g, b, s, dO, _ = R.inputs(2, 700, 200, torch.float32, True, True, 0.1, seed=12)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
+    big = torch.ones(1 << 28, device="cuda")
+    total = torch.zeros((), device="cuda")
+    for _ in range(20):                                     # a queue of work on the caller's stream
+        big.mul_(1.0)
+    old = [torch.full_like(x, 7.0) for _ in range(8)]
+    for t in old:
+        total += t.sum()
+    del old, t                                              # free to torch, still to be read
     o, hT, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True, stream=side)
     gr = ops.linrec_bwd(x, g, st, dO, beta=b, stream=side)
-    junk = [torch.full_like(x, 7.0) for _ in range(4)]      # must not land in memory still in use there
+    step = ops.linrec_step(x[:, 0].contiguous(), g[:, 0].contiguous(), s.clone(), stream=torch.cuda.current_stream())
     side.synchronize()
     h, err = R.states_and_bounds(x, g, b, s)
     R.check("o", o, h[:, 1:], err[:, 1:])
     for n, (v, e) in R.grads_and_bounds(x, g, b, s, dO, None).items():
         R.check(n, gr[n], v, e)
-    assert all(bool((j == 7.0).all()) for j in junk)
+    assert total.item() == 7.0 * 8 * x.numel()
+    h1, err1 = R.states_and_bounds(x[:, :1], g[:, :1], None, s)
+    R.check("o", step, h1[:, 1], err1[:, 1])
 
 
 def test_captured_and_replayed():
@@ -288,6 +300,34 @@ def test_training_step_in_a_graph():
         ref = R.grads_and_bounds(*new)
         for n, got in zip(("dx", "dg", "dbeta", "dh0"), grads):
             R.check(n, got, *ref[n])
+
+
+def test_whole_numbers_are_exact_over_many_tiles():
+    """With g = 0 the states are running sums: of whole numbers, exact however the tiles
+    are joined, over thousands of tiles, forwards and backwards."""
+    B, T, D = 2, 1000003, 5
+    announce("linrec_exact", B, T, D)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    x = torch.randint(-2, 3, (B, T, D), generator=gen, device="cuda").float()
+    g = torch.zeros_like(x)
+    h0 = torch.randint(-9, 9, (B, D), generator=gen, device="cuda").float()
+    o, hT, st = ops.linrec_fwd(x, g, h0=h0, want_states=True)
+    h = torch.cumsum(x.double(), 1) + h0.double()[:, None]
+    assert torch.equal(o.double(), h) and torch.equal(hT.double(), h[:, -1])
+    assert torch.equal(st[:, 0], h0) and torch.equal(st[:, 1:].double(), h[:, 15:-1:16])
+    gr = ops.linrec_bwd(x, g, st, x, dh_T=h0)
+    e = torch.cumsum(x.double().flip(1), 1).flip(1) + h0.double()[:, None]
+    assert torch.equal(gr["dx"].double(), e) and torch.equal(gr["dh0"].double(), e[:, 0])
+
+
+def test_second_derivatives_are_refused():
+    x, g, b, s, dO, dhT = R.inputs(1, 20, 4, torch.float32, seed=22)
+    x.requires_grad_(True)
+    o, _ = linear_recurrence(x, g, b, s)
+    (gx,) = torch.autograd.grad(o.square().sum(), [x], create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(gx.sum(), [x])
 
 
 def test_more_than_2_to_the_31_elements():
