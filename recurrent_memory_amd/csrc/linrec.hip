@@ -41,7 +41,7 @@ constexpr int kGroup = 16;          // tiles from one published state to the nex
 constexpr int kCarryWave = kMaxWaves - 1;   // the last wave collects the state, the others maps,
 constexpr int kPer = (kGroup - 1 + kMaxWaves - 2) / (kMaxWaves - 1);   // this many each
 constexpr int kStepThreads = 256;
-constexpr uint32_t kMaxGrid = 1u << 20;
+constexpr uint32_t kMaxGrid = 1u << 16;   // workgroups; with more tiles than that, each takes several
 
 // Memory accesses of the tiles.  NT: non-temporal, where rows are whole cache lines and
 // every line passes once (B=1 T=32768 D=2048 bf16: forward 109 us plain, 102 us

@@ -321,6 +321,24 @@ def test_whole_numbers_are_exact_over_many_tiles():
     assert torch.equal(gr["dx"].double(), e) and torch.equal(gr["dh0"].double(), e[:, 0])
 
 
+@pytest.mark.parametrize("B,T,D", [(5, 3, 1000003), (2, 257, 720001)])
+def test_more_tiles_than_workgroups(B, T, D):
+    """Over 65536 tiles a workgroup takes several, of one tile a sequence and of three."""
+    announce("linrec_many_tiles", B, T, D)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    x = torch.randint(-2, 3, (B, T, D), generator=gen, device="cuda").float()
+    g = torch.zeros_like(x)
+    o, hT, st = ops.linrec_fwd(x, g, want_states=True)
+    h = torch.cumsum(x.double(), 1)
+    assert torch.equal(o, h.float()) and torch.equal(hT, h[:, -1].float())
+    assert torch.equal(st[:, 1:], h[:, 15:-1:16].float()) and not bool(st[:, 0].any())
+    gr = ops.linrec_bwd(x, g, st, x)
+    e = torch.cumsum(x.double().flip(1), 1).flip(1)
+    assert torch.equal(gr["dx"], e.float()) and torch.equal(gr["dh0"], e[:, 0].float())
+    assert torch.equal(gr["dg"], (e * torch.cat((torch.zeros_like(h[:, :1]), h[:, :-1]), 1)).float())
+
+
 def test_second_derivatives_are_refused():
     x, g, b, s, dO, dhT = R.inputs(1, 20, 4, torch.float32, seed=22)
     x.requires_grad_(True)
