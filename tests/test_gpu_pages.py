@@ -54,7 +54,7 @@ LISTS = [
 ]
 
 
-@pytest.mark.parametrize("page", [1, 3, 4, 64, 1001, 8192, 8196, 70000])
+@pytest.mark.parametrize("page", [1, 3, 4, 64, 127, 512, 516, 1001, 8192, 8196, 70000])
 def test_copy_lists(page):
     announce("pages_copy", page)
     for i, (N, dst, src) in enumerate(LISTS):
