@@ -168,7 +168,7 @@ def test_in_place_state_and_chunked_prefill():
     R.check("o", o, h[:, 1:], err[:, 1:])
 
 
-@pytest.mark.parametrize("B,T,D", [(2, 3000, 300), (4, 100, 64)])
+@pytest.mark.parametrize("B,T,D", [(2, 3000, 300), (4, 100, 64), (1, 16384, 2048)])
 def test_same_results_on_every_run(B, T, D):
     """Bitwise, also while another stream runs the same operator."""
     announce("linrec_deterministic", B, T, D)
