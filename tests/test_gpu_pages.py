@@ -123,19 +123,27 @@ def test_lists_that_are_parts_of_longer_ones():
 
 
 def test_decode_slots_streams_large_pools():
-    """From 128 MiB of states on the accesses are non-temporal: the same bits."""
+    """From 128 MiB of states on the accesses are non-temporal: the same bits, also for
+    pages that several rows share."""
     announce("decode_slots_large")
     for variant in ("gdn", "kda"):
         B, H = 130, 16
         t = _step_inputs(variant, "bf16", B, H, 128, 128, seed=9)
         pool = 0.02 * torch.randn(140, H, 128, 128, device="cuda")
-        slots = torch.randperm(140, generator=torch.Generator().manual_seed(3))[:B].to(torch.int32).cuda()
-        S, want = pool[slots.long()].contiguous(), pool.clone()
-        o = ops.delta_decode_slots(variant, t["q"], t["k"], t["v"], t["beta"], pool, slots, g=t["g"])
-        ow = ops.delta_decode(variant, t["q"], t["k"], t["v"], t["beta"], S, g=t["g"])
-        want[slots.long()] = S
-        torch.cuda.synchronize()
-        assert torch.equal(o, ow) and torch.equal(pool, want)
+        want = pool.clone()
+        slots = torch.randperm(140, generator=torch.Generator().manual_seed(3))[:B]
+        slots[64], slots[129], slots[128] = slots[0], slots[0], slots[7]
+        o = ops.delta_decode_slots(variant, t["q"], t["k"], t["v"], t["beta"], pool, slots.to(torch.int32).cuda(),
+                                   g=t["g"])
+        turns = [[b for b in range(B) if b not in (64, 128, 129)], [64, 128], [129]]
+        for rows in turns:
+            at = slots[rows].cuda()
+            a = {n: v[rows].contiguous() for n, v in t.items() if v is not None}
+            S = want[at].contiguous()
+            ow = ops.delta_decode(variant, a["q"], a["k"], a["v"], a["beta"], S, g=a["g"])
+            want[at] = S
+            assert torch.equal(o[rows], ow)
+        assert torch.equal(pool, want)
 
 
 def test_copy_keeps_bit_patterns():
@@ -290,6 +298,42 @@ def test_decode_slots_many_rows():
         want[st[rows].long()] = S
         assert torch.equal(o[rows], ow)
     assert torch.equal(pool, want)
+
+
+def test_token_steps_captured_and_replayed():
+    """A captured decode step follows its slots and inputs from replay to replay, with
+    eager work in between."""
+    announce("decode_slots_graph")
+    B, H, N = 4, 2, 9
+    t = _step_inputs("gdn", "bf16", B, H, 64, 128, seed=11)
+    pool = 0.02 * torch.randn(N, H, 128, 64, device="cuda")
+    h, x = torch.randn(N, 40, device="cuda"), torch.randn(B, 40, device="cuda")
+    z = torch.zeros_like(x)
+    slots = _ints([0, 1, 2, -1])
+    o, oh = torch.zeros(B, H, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, 40, device="cuda")
+
+    def run(pool, h, o, oh):
+        ops.delta_decode_slots("gdn", t["q"], t["k"], t["v"], t["beta"], pool, slots, g=t["g"], o=o)
+        ops.linrec_step(x, z, h, slots=slots, o=oh)
+
+    run(pool.clone(), h.clone(), o.clone(), oh.clone())
+    torch.cuda.synchronize()
+    gph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gph):
+        run(pool, h, o, oh)
+    for i, rows in enumerate(([0, 1, 2, -1], [8, 8, 3, 8], [-1, -1, 5, 99], [2, 0, 1, 4])):
+        new = _step_inputs("gdn", "bf16", B, H, 64, 128, seed=20 + i)
+        for n in t:
+            if t[n] is not None:
+                t[n].copy_(new[n])
+        x.copy_(torch.randn(B, 40, device="cuda"))
+        slots.copy_(_ints(rows))
+        want = [v.clone() for v in (pool, h, o, oh)]
+        run(*want)
+        gph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((pool, h, o, oh), want):
+            assert torch.equal(a, b), i
 
 
 def test_refusals():
