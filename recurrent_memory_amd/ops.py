@@ -468,6 +468,13 @@ def _dtype_code(t: torch.Tensor) -> int:
     return code
 
 
+def _fits(*sizes):
+    """Refuses sizes past 32 bits as the library refuses those past its limits: ctypes
+    would hand them on modulo 2^32."""
+    if max(sizes) >= 1 << 31:
+        _raise(2)
+
+
 _current_gpu = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -527,6 +534,7 @@ def _linrec_check(x, g, beta, dims: int):
     code = _dtype_code(x)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
+    _fits(*shape)
     _need("g", g, shape, dt, gpu)
     if beta is not None:
         _need("beta", beta, shape, dt, gpu)
@@ -629,6 +637,7 @@ def linrec_step(x: torch.Tensor, g: torch.Tensor, h: torch.Tensor, beta: Optiona
     if h.dim() != 2:
         raise ValueError(f"h: expected 2 dimensions, got shape {tuple(h.shape)}")
     pages = h.shape[0]
+    _fits(pages)
     _need("h", h, (B if slots is None else pages, D), torch.float32, gpu)
     if slots is not None:
         _need("slots", slots, (B,), torch.int32, gpu)
@@ -690,6 +699,7 @@ def _page(name: str, t: torch.Tensor, gpu) -> int:
     if len(shape) < 2:
         raise ValueError(f"{name}: expected [n_pages, ...], got shape {tuple(shape)}")
     _need(name, t, shape, torch.float32, gpu)
+    _fits(shape[0])
     return t.numel() // shape[0] if shape[0] else 0
 
 
@@ -709,6 +719,7 @@ def pages_copy(pool: torch.Tensor, dst: torch.Tensor, src: torch.Tensor,
     elif _page("src_pool", src_pool, gpu) != page:
         raise ValueError(f"src_pool: pages of {tuple(src_pool.shape[1:])}, expected {tuple(pool.shape[1:])}")
     n = dst.numel()
+    _fits(n)
     _need("dst", dst, (n,), torch.int32, gpu)
     _need("src", src, (n,), torch.int32, gpu)
     _enqueue(gpu, lib.delta_pages_copy, PagesDesc(page, pool.shape[0], n), pool.data_ptr(), dst.data_ptr(),
@@ -728,6 +739,7 @@ def pages_compact(pool: torch.Tensor, slots: torch.Tensor, slots_out: Optional[t
     gpu = _gpu("pool", pool)
     page = _page("pool", pool, gpu)
     n = slots.numel()
+    _fits(n)
     _need("slots", slots, (n,), torch.int32, gpu)
     if slots_out is None:
         slots_out = torch.empty_like(slots)

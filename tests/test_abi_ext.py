@@ -4,6 +4,7 @@ import ctypes
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 from recurrent_memory_amd import autograd, ops
 
@@ -193,3 +194,34 @@ def test_binding_refuses_cpu_tensors():
                  lambda: ops.delta_decode_slots("gdn", x, x, x, x, x, x), lambda: autograd.linear_recurrence(x, x)):
         with pytest.raises(ValueError, match="GPU tensor"):
             call()
+
+
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32, 2 ** 32 + 2, 2 ** 33 + 3])
+def test_binding_refuses_sizes_past_32_bits(past):
+    """Descriptors hold 32-bit sizes, and ctypes masks what does not fit: 2^32 + 2 tokens
+    must not be taken as 2.  Tensors without storage, so that nothing is allocated."""
+    with FakeTensorMode():
+        def f32(*shape):
+            return torch.empty(shape, device="cuda")
+
+        def i32(n):
+            return torch.empty(n, dtype=torch.int32, device="cuda")
+
+        row, pool = f32(2, 1), f32(4, 8)
+        calls = []
+        for shape in ((past, 1, 1), (1, past, 1), (1, 1, past)):
+            y = f32(*shape)
+            st = f32(shape[0], -(-shape[1] // ops.LINREC_BLOCK), shape[2])
+            calls += [lambda y=y: ops.linrec_fwd(y, y, o=y, want_state=False), lambda y=y, st=st: ops.linrec_bwd(
+                y, y, st, y, want_dh0=False, out=dict(dx=y, dg=y))]
+        for y in (f32(past, 1), f32(1, past)):
+            calls.append(lambda y=y: ops.linrec_step(y, y, y, o=y))
+        calls += [lambda: ops.linrec_step(row, row, f32(past, 1), slots=i32(2), o=row),
+                  lambda: ops.pages_copy(f32(past, 8), i32(2), i32(2)), lambda: ops.pages_copy(pool, i32(past), i32(past)),
+                  lambda: ops.pages_copy(pool, i32(2), i32(2), src_pool=f32(past, 8)),
+                  lambda: ops.pages_compact(f32(past, 8), i32(2), slots_out=i32(2), n_live=i32(1)),
+                  lambda: ops.pages_compact(pool, i32(past), slots_out=i32(past), n_live=i32(1))]
+        for n, call in enumerate(calls):
+            with pytest.raises(ops.DeltaRuleError) as e:
+                call()
+            assert e.value.status == DR_E_SHAPE, n
