@@ -26,6 +26,14 @@ from torch.autograd.function import once_differentiable
 from . import ops
 
 
+def _gradient(t: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """A gradient as the library takes it: contiguous, of ``dtype``, at a multiple of 16
+    bytes.  torch hands out contiguous gradients at any address (a part of the gradient
+    of a ``cat`` or ``stack``)."""
+    t = t.contiguous().to(dtype)
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _DeltaRule(torch.autograd.Function):
     @staticmethod
     def forward(ctx, variant, q, k, v, beta, g, wgate, S0):
@@ -39,9 +47,9 @@ class _DeltaRule(torch.autograd.Function):
         q, k, v, beta, g, wgate, S0 = ctx.saved_tensors
         if dO is None:
             dO = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
-        dO = dO.contiguous().to(v.dtype)
+        dO = _gradient(dO, v.dtype)
         if dS_T is not None:
-            dS_T = dS_T.contiguous().to(torch.float32)
+            dS_T = _gradient(dS_T, torch.float32)
         gr = ops.delta_bwd(ctx.variant, q, k, v, beta, dO, g=g, S0=S0, dS_T=dS_T, wgate=wgate,
                            want_dS0=S0 is not None and ctx.needs_input_grad[7])
         return (None, gr["dq"], gr["dk"], gr["dv"], gr["dbeta"], gr["dg"], gr["dwgate"], gr["dS0"])
@@ -66,8 +74,8 @@ class _LinearRecurrence(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dO, dh_T):
         x, g, beta, states = ctx.saved_tensors
-        gr = ops.linrec_bwd(x, g, states, dO.contiguous().to(x.dtype), beta=beta,
-                            dh_T=dh_T.contiguous().to(torch.float32), want_dh0=ctx.needs_input_grad[3])
+        gr = ops.linrec_bwd(x, g, states, _gradient(dO, x.dtype), beta=beta, dh_T=_gradient(dh_T, torch.float32),
+                            want_dh0=ctx.needs_input_grad[3])
         return gr["dx"], gr["dg"], gr["dbeta"], gr["dh0"]
 
 

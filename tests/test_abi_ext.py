@@ -225,3 +225,30 @@ def test_binding_refuses_sizes_past_32_bits(past):
             with pytest.raises(ops.DeltaRuleError) as e:
                 call()
             assert e.value.status == DR_E_SHAPE, n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("join", [torch.cat, torch.stack])
+def test_gradients_are_taken_at_any_address(join, dtype):
+    """The gradients that torch hands to the outputs of a joined tensor are contiguous parts
+    of one buffer; the library takes them at multiples of 16 bytes."""
+    parts = [torch.zeros(3, 7, 5, dtype=dtype, requires_grad=True) for _ in range(4)]
+    seen = []
+
+    class Same(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, t):
+            return t.clone()
+
+        @staticmethod
+        def backward(ctx, grad):
+            seen.append((grad, autograd._gradient(grad, dtype)))
+            return grad
+
+    whole = join([Same.apply(p) for p in parts])
+    whole.backward(torch.arange(whole.numel(), dtype=dtype).view_as(whole))
+    assert any(given.is_contiguous() and given.data_ptr() % 16 for given, _ in seen)
+    for given, taken in seen:
+        assert torch.equal(given, taken) and taken.is_contiguous() and taken.data_ptr() % 16 == 0
+    even = torch.zeros(4, 4, dtype=dtype)
+    assert autograd._gradient(even, dtype) is even                        # nothing copied without need

@@ -199,6 +199,31 @@ def test_autograd_function(variant):
     _check(variant, "f32", {n: (None if t is None else host(t)) for n, t in got.items()}, ref)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_autograd_takes_gradients_at_any_address(dtype):
+    """o and S_T joined behind three other values: their gradients start inside a buffer,
+    and give the same bits as gradients that start at one."""
+    from recurrent_memory_amd.autograd import delta_rule
+    announce("autograd_joined", dtype)
+    w = Workload("t", "gdn", dtype, B=1, H=2, T=70, dk=64, dv=64, random_s0=True, seed=49)
+    x = make_forward_inputs(w)
+    dO, dST = (dev(t, d) for t, d in zip(_upstream(w, 16), (dtype, "f32")))
+    leaves = {n: dev(x[n], dtype).requires_grad_(True) for n in ("q", "k", "v", "beta", "g")}
+    leaves["S0"] = dev(x["S0"]).requires_grad_(True)
+
+    def grads(joined):
+        o, S = delta_rule("gdn", leaves["q"], leaves["k"], leaves["v"], leaves["beta"], g=leaves["g"], S0=leaves["S0"])
+        if not joined:
+            return torch.autograd.grad((o, S), list(leaves.values()), (dO, dST))
+        three = [torch.zeros(3, dtype=t.dtype, device="cuda", requires_grad=True) * 1 for t in (o, S)]
+        whole = [torch.cat((z, t.flatten())) for z, t in zip(three, (o, S))]
+        return torch.autograd.grad(whole, list(leaves.values()),
+                                   [torch.cat((torch.zeros_like(z), t.flatten())) for z, t in zip(three, (dO, dST))])
+
+    for n, a, b in zip(leaves, grads(False), grads(True)):
+        assert torch.equal(a, b), n
+
+
 @pytest.mark.parametrize("variant", VARS)
 def test_bwd_many_heads(variant):
     """B*H = 330 heads: the chain kernels' XCD-aware head map with a partial last

@@ -271,6 +271,25 @@ def test_autograd(dtype, with_beta, with_h0):
     assert not o.requires_grad
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("join", [torch.cat, torch.stack])
+def test_gradients_at_any_address(dtype, join):
+    """Two sequences' outputs joined: the second one's gradients start inside a buffer."""
+    announce("linrec_autograd_joined", dtype, join.__name__)
+    sets = [R.inputs(3, 7, 5, DT[dtype], True, True, 0.3, seed=60 + i) for i in range(2)]
+    leaves, os, hs = [], [], []
+    for x, g, b, s, _, _ in sets:
+        leaves.append([t.requires_grad_(True) for t in (x, g, b, s)])
+        o, hT = linear_recurrence(x, g, b, s)
+        os.append(o), hs.append(hT)
+    grads = torch.autograd.grad((join(os), join(hs)), sum(leaves, []),
+                                (join([v[4] for v in sets]), join([v[5] for v in sets])))
+    for i, (x, g, b, s, dO, dhT) in enumerate(sets):
+        ref = R.grads_and_bounds(*(t.detach() for t in (x, g, b, s)), dO, dhT)
+        for n, got in zip(("dx", "dg", "dbeta", "dh0"), grads[4 * i:]):
+            R.check(n, got, *ref[n])
+
+
 def test_training_step_in_a_graph():
     """Forward and torch.autograd.grad captured together and replayed on new inputs."""
     announce("linrec_autograd_graph")
