@@ -34,10 +34,13 @@ int dr_ext_version(void);
  *
  * with a log-decay g_t <= 0 and a write gate beta_t per channel and token.  It
  * is the delta rule's decay and write without the read that makes a matrix
- * memory error-correcting.  g = -inf forgets everything before its token (a
- * document's border in a packed sequence); there is no floor.  g > 0 is not
- * refused, but the decays of up to 384 consecutive tokens are multiplied up, and
- * their product must stay inside fp32.  Tokens with g = 0 and x = 0 leave the
+ * memory error-correcting.  A decay that is zero in fp32 (g = -inf; any g below
+ * -87.4) forgets everything before its token, infinities and NaN too (a
+ * document's border in a packed sequence), and lets no gradient past it, whatever
+ * arrives: dg is 0 there.  Elsewhere an infinity or NaN stays in its channel, as
+ * the formula has it.  There is no floor.  g > 0 is not refused, but the decays of
+ * up to 384 consecutive tokens are multiplied up, and their product must stay
+ * inside fp32.  Tokens with g = 0 and x = 0 leave the
  * state as it is (the padding of a short sequence in a batch).
  *
  * States, decays and sums are fp32 whatever the dtype; o and the gradients are

@@ -18,6 +18,15 @@
 // such state and at most 15 maps.  Which values are joined in which order depends on
 // positions alone, so results do not depend on timing.
 //
+// Forgetting.  A decay that is zero in fp32 drops the state in front of it, whatever that
+// is: 0 times an infinity would be NaN.  So does the map of a run that holds such a token;
+// a product of decays that only gets small stops at the smallest normal number instead
+// (which moves a state by at most 2^-126 of one before it), so that an infinity stays one.
+// A wave takes its 16 tokens without regard to this, and only if their product of decays
+// leaves the normal numbers in some lane again, with a selection for each token
+// (selections in every wave: backward 181 instead of 170 us at B=1 T=32768 D=2048 bf16; the
+// registers that the second form spills are spilled in that form only).
+//
 // Waiting.  A published word carries its own readiness: the workspace is filled with
 // all-ones (a NaN pattern that is never published) before the launch, and readers poll
 // the word itself with relaxed device-scope atomics, so no fence or flag is needed.
@@ -27,6 +36,8 @@
 // waits; by induction over the column every wait ends, whatever else runs on the GPU.
 // (One counter for all columns hands out a tile every 20 ns at best, 50 tiles a
 // microsecond, which is as much as HBM takes.)
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "slots.h"
@@ -41,7 +52,12 @@ constexpr int kGroup = 16;          // tiles from one published state to the nex
 constexpr int kCarryWave = kMaxWaves - 1;   // the last wave collects the state, the others maps,
 constexpr int kPer = (kGroup - 1 + kMaxWaves - 2) / (kMaxWaves - 1);   // this many each
 constexpr int kStepThreads = 256;
+constexpr float kSmallest = 0x1p-126f;
 constexpr uint32_t kMaxGrid = 1u << 16;   // workgroups; with more tiles than that, each takes several
+
+// A map applied to a state, and the decays of adjacent runs joined (see Forgetting).
+__device__ __forceinline__ float apply(float a, float h, float c) { return a == 0.f ? c : fmaf(a, h, c); }
+__device__ __forceinline__ float join(float A, float a) { return A == 0.f || a == 0.f ? 0.f : fmaxf(A * a, kSmallest); }
 
 // Memory accesses of the tiles.  NT: non-temporal, where rows are whole cache lines and
 // every line passes once (B=1 T=32768 D=2048 bf16: forward 109 us plain, 102 us
@@ -166,8 +182,8 @@ __device__ __forceinline__ void collect_maps(const uint64_t* at, int64_t stride,
         for (int i = 0; i < kPer; ++i) {
             if (i < n) {
                 const float a = __uint_as_float(static_cast<uint32_t>(m[i][v] >> 32));
-                c = fmaf(a, c, __uint_as_float(static_cast<uint32_t>(m[i][v])));
-                A *= a;
+                c = apply(a, c, __uint_as_float(static_cast<uint32_t>(m[i][v])));
+                A = join(A, a);
             }
         }
         out[v] = make_float2(A, c);
@@ -233,8 +249,8 @@ __device__ __forceinline__ void wave_start(Joint<VEC>& J, const Tiles& ts, int w
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float2 m = J.wave[k][lane * VEC + v];
-                    c[v] = fmaf(m.x, c[v], m.y);
-                    A[v] *= m.x;
+                    c[v] = apply(m.x, c[v], m.y);
+                    A[v] = join(A[v], m.x);
                 }
             }
             if (q == 0) {
@@ -264,21 +280,21 @@ __device__ __forceinline__ void wave_start(Joint<VEC>& J, const Tiles& ts, int w
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float2 m = J.tile[k][lane * VEC + v];
-            h[v] = fmaf(m.x, h[v], m.y);
+            h[v] = apply(m.x, h[v], m.y);
         }
     }
     if (ts.chain > 1 && w == kCarryWave && more && j == kGroup - 1) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
             if (v < nch)
-                __hip_atomic_store(ts.after + (q / kGroup) * channels + ch + v, published(fmaf(A[v], h[v], c[v])),
+                __hip_atomic_store(ts.after + (q / kGroup) * channels + ch + v, published(apply(A[v], h[v], c[v])),
                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     for (int k = 0; k < pos; ++k) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float2 m = J.wave[k][lane * VEC + v];
-            h[v] = fmaf(m.x, h[v], m.y);
+            h[v] = apply(m.x, h[v], m.y);
         }
     }
 }
@@ -366,6 +382,15 @@ __device__ __forceinline__ void forget_derived(uint32_t* r) {
     for (int i = 0; i < kTok; ++i) asm volatile("" : "+v"(r[i]));
 }
 
+// Whether a token of the wave may forget, from the products of its lanes' decays.
+template <int VEC>
+__device__ __forceinline__ bool any_forgets(const float* A) {
+    bool normal = true;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) normal = normal && A[v] >= kSmallest;
+    return __any(!normal);
+}
+
 template <typename W, bool BETA, bool UNI, bool NT>
 __global__ __launch_bounds__(kSingleWaves * 64) void linrec_fwd_kernel(LinrecArgs p, Tiles ts) {
     constexpr int VEC = W::VEC;
@@ -398,17 +423,28 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_fwd_kernel(LinrecArg
                 if constexpr (BETA) u[v] *= b[v];
             }
         };
-        float A[VEC], h[VEC], a[VEC], u[VEC];
+        float A[VEC], h[VEC];
+        auto reduce = [&](auto forgets) {
+            float a[VEC], u[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; h[v] = 0.f; }
+            for (int v = 0; v < VEC; ++v) { A[v] = 1.f; h[v] = 0.f; }
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            token(i, a, u);
+            for (int i = 0; i < kTok; ++i) {
+                token(i, a, u);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                h[v] = fmaf(a[v], h[v], u[v]);
-                A[v] *= a[v];
+                for (int v = 0; v < VEC; ++v) {
+                    h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                    A[v] = forgets ? join(A[v], a[v]) : A[v] * a[v];
+                }
             }
+        };
+        reduce(std::false_type());
+        const bool forgets = any_forgets<VEC>(A);
+        if (__builtin_expect(forgets, 0)) {
+            forget_derived(gr);
+            forget_derived(xr);
+            if constexpr (BETA) forget_derived(br);
+            reduce(std::true_type());
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) J.wave[w][lane * VEC + v] = make_float2(A[v], h[v]);
@@ -424,12 +460,23 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_fwd_kernel(LinrecArg
                 if (v < at.nch) s[v] = h[v];
         }
         typename W::T* o = static_cast<typename W::T*>(p.o) + row;
+        auto finish = [&](auto forgets) {
+            float a[VEC], u[VEC];
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            token(i, a, u);
+            for (int i = 0; i < kTok; ++i) {
+                token(i, a, u);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[v], h[v], u[v]);
-            if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+                for (int v = 0; v < VEC; ++v) h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+            }
+        };
+        if (__builtin_expect(forgets, 0)) {
+            forget_derived(gr);
+            forget_derived(xr);
+            if constexpr (BETA) forget_derived(br);
+            finish(std::true_type());
+        } else {
+            finish(std::false_type());
         }
         // beyond the last token h is carried along unchanged
         if (p.hT != nullptr && t0 + n == p.T) {
@@ -472,18 +519,29 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwd
 #pragma unroll
             for (int v = 0; v < VEC; ++v) a[v] = __expf(a[v]);
         };
-        float A[VEC], r[VEC], a[VEC], d[VEC];
+        float A[VEC], r[VEC];
+        auto reduce = [&](auto forgets) {
+            float a[VEC], d[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; r[v] = 0.f; }
+            for (int v = 0; v < VEC; ++v) { A[v] = 1.f; r[v] = 0.f; }
 #pragma unroll
-        for (int i = kTok - 1; i >= 0; --i) {
-            decay(i, a);
-            W::unpack(dr[i], d);
+            for (int i = kTok - 1; i >= 0; --i) {
+                decay(i, a);
+                W::unpack(dr[i], d);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                r[v] = a[v] * (r[v] + d[v]);
-                A[v] *= a[v];
+                for (int v = 0; v < VEC; ++v) {
+                    const float e = r[v] + d[v];
+                    r[v] = forgets ? apply(a[v], e, 0.f) : a[v] * e;
+                    A[v] = forgets ? join(A[v], a[v]) : A[v] * a[v];
+                }
             }
+        };
+        reduce(std::false_type());
+        const bool forgets = any_forgets<VEC>(A);
+        if (__builtin_expect(forgets, 0)) {
+            forget_derived(gr);
+            forget_derived(dr);
+            reduce(std::true_type());
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) J.wave[pos][lane * VEC + v] = make_float2(A[v], r[v]);
@@ -495,66 +553,77 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwd
         // every fourth token first, then, from the last four tokens to the first, the
         // ones between (all sixteen at once do not fit beside the inputs in 128 registers).
         typedef typename W::T T;
-        auto advance = [&](int i) {
-            float u[VEC], b[VEC];
-            decay(i, a);
-            W::unpack(xr[i], u);
-            if constexpr (BETA) W::unpack(br[i], b);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if constexpr (BETA) u[v] *= b[v];
-                h[v] = fmaf(a[v], h[v], u[v]);
-            }
-        };
-        constexpr int kPart = 4;
-        float start[kTok / kPart][VEC];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            if (i % kPart == 0) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
-            }
-            if (i < kTok - kPart) advance(i);
-        }
-#pragma unroll
-        for (int part = kTok / kPart - 1; part >= 0; --part) {
-            float before[kPart][VEC];
-            forget_derived(gr);
-            forget_derived(xr);
-            if constexpr (BETA) forget_derived(br);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
-                if (i + 1 < kPart) advance(part * kPart + i);
-            }
-#pragma unroll
-            for (int j = kPart - 1; j >= 0; --j) {
-                const int i = part * kPart + j;
-                float e[VEC], x[VEC], b[VEC], dg[VEC];
+        auto finish = [&](auto forgets) {
+            auto advance = [&](int i) {
+                float a[VEC], u[VEC], b[VEC];
                 decay(i, a);
-                W::unpack(dr[i], e);
-                W::unpack(xr[i], x);
+                W::unpack(xr[i], u);
                 if constexpr (BETA) W::unpack(br[i], b);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    e[v] += r[v];
-                    r[v] = a[v] * e[v];
-                    dg[v] = r[v] * before[j][v];
-                    if constexpr (BETA) {
-                        x[v] *= e[v];
-                        e[v] *= b[v];
+                    if constexpr (BETA) u[v] *= b[v];
+                    h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                }
+            };
+            constexpr int kPart = 4;
+            float start[kTok / kPart][VEC];
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                if (i % kPart == 0) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
+                }
+                if (i < kTok - kPart) advance(i);
+            }
+#pragma unroll
+            for (int part = kTok / kPart - 1; part >= 0; --part) {
+                float before[kPart][VEC];
+                forget_derived(gr);
+                forget_derived(xr);
+                if constexpr (BETA) forget_derived(br);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
+                    if (i + 1 < kPart) advance(part * kPart + i);
+                }
+#pragma unroll
+                for (int j = kPart - 1; j >= 0; --j) {
+                    const int i = part * kPart + j;
+                    float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
+                    decay(i, a);
+                    W::unpack(dr[i], e);
+                    W::unpack(xr[i], x);
+                    if constexpr (BETA) W::unpack(br[i], b);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        e[v] += r[v];
+                        r[v] = forgets ? apply(a[v], e[v], 0.f) : a[v] * e[v];
+                        dg[v] = forgets ? apply(a[v], before[j][v] * e[v], 0.f) : r[v] * before[j][v];
+                        if constexpr (BETA) {
+                            x[v] *= e[v];
+                            e[v] *= b[v];
+                        }
+                    }
+                    if (i < n) {
+                        const int64_t el = row + static_cast<int64_t>(i) * p.D;
+                        W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
+                        W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
+                        if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
                     }
                 }
-                if (i < n) {
-                    const int64_t el = row + static_cast<int64_t>(i) * p.D;
-                    W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
-                    W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
-                    if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
-                }
             }
+        };
+        if (__builtin_expect(forgets, 0)) {
+            forget_derived(gr);
+            forget_derived(xr);
+            forget_derived(dr);
+            if constexpr (BETA) forget_derived(br);
+            finish(std::true_type());
+        } else {
+            finish(std::false_type());
         }
         if (p.dh0 != nullptr && t0 == 0) {
 #pragma unroll
@@ -621,7 +690,7 @@ __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArg
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if constexpr (BETA) u[v] *= w[v];
-                h[v] = fmaf(__expf(a[v]), h[v], u[v]);
+                h[v] = apply(__expf(a[v]), h[v], u[v]);
             }
             store_channels<E, V>(p.o, at, h);
         }

@@ -108,6 +108,84 @@ def test_non_finite_stays_in_its_channel(dtype, value):
     assert torch.equal(g1["dh0"][rest], g0["dh0"][rest]) and not bool(torch.isfinite(g1["dh0"][1, 77]))
 
 
+BAD = [float("inf"), -float("inf"), float("nan")]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("border,at", [(1, 0), (20, 3), (20, 19), (33, 16), (130, 127), (256, 0), (700, 690), (2200, 5)])
+def test_a_border_stops_what_is_not_finite(dtype, border, at):
+    """Nothing passes a token that forgets: an infinity or NaN written or handed in before
+    it, or arriving as a gradient after it, changes no bit on its other side."""
+    announce("linrec_border", dtype, border, at)
+    B, T, D = 1, border + 300, 66
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], True, True, 0.1, seed=border)
+    g[:, border, ::2] = -float("inf")
+    g[:, border, 1::2] = -88.0                               # zero in fp32 too
+    want = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+    wgr = ops.linrec_bwd(x, g, want[2], dO, beta=b, dh_T=dhT)
+    blocks = -(-border // 16) if border % 16 else border // 16 + 1      # states of tokens behind the border
+    for i, bad in enumerate(BAD):
+        x1, s1 = x.clone(), s.clone()
+        x1[0, at, i::6] = bad
+        s1[0, i + 3::6] = bad
+        o, hT, st = ops.linrec_fwd(x1, g, beta=b, h0=s1, want_states=True)
+        assert torch.equal(o[:, border:], want[0][:, border:]) and torch.equal(hT, want[1])
+        assert torch.equal(st[:, blocks:], want[2][:, blocks:])
+        assert not bool(torch.isfinite(o[:, at:border, i::6]).any())
+        gr = ops.linrec_bwd(x1, g, st, dO, beta=b, dh_T=dhT)
+        for n in ("dx", "dg", "dbeta"):
+            assert torch.equal(gr[n][:, border:], wgr[n][:, border:]), n
+        assert torch.equal(gr["dx"], wgr["dx"]) and torch.equal(gr["dh0"], wgr["dh0"])
+        dO1, dhT1 = dO.clone(), dhT.clone()
+        dO1[0, border + 1 + at % 200, i::6] = bad
+        dhT1[0, i + 3::6] = bad
+        gr = ops.linrec_bwd(x, g, want[2], dO1, beta=b, dh_T=dhT1)
+        for n in ("dx", "dg", "dbeta"):
+            assert torch.equal(gr[n][:, :border], wgr[n][:, :border]), n
+        assert torch.equal(gr["dh0"], wgr["dh0"])
+        assert not bool(gr["dg"][:, border].any())
+        assert not bool(torch.isfinite(gr["dx"][:, border, i::6]).any())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("g0", [-0.5, -9.0, -80.0])
+def test_an_infinity_outlives_small_decays(dtype, g0):
+    """However small the product of decays gets, an infinity stays what it is, forwards
+    and backwards: only a decay of zero ends it."""
+    announce("linrec_inf", dtype, g0)
+    x, _, b, s, dO, dhT = R.inputs(1, 2500, 34, DT[dtype], True, True, 1.0, seed=70)
+    g = torch.full_like(x, g0)
+    x1, s1 = x.clone(), s.clone()
+    x1[0, 7, 0], x1[0, 140, 1], s1[0, 2] = float("inf"), -float("inf"), float("inf")
+    o, hT, st = ops.linrec_fwd(x1, g, beta=b, h0=s1, want_states=True)
+    for c, t, v in ((0, 7, float("inf")), (1, 140, -float("inf")), (2, 0, float("inf"))):
+        assert bool((o[0, t:, c] == v).all()) and hT[0, c] == v
+        assert bool((st[0, t // 16 + 1:, c] == v).all())
+    h, err = R.states_and_bounds(x, g, b, s)
+    R.check("o", o[:, :, 3:], h[:, 1:, 3:], err[:, 1:, 3:])
+    dO1, dhT1 = dO.clone(), dhT.clone()
+    dO1[0, 2490, 0], dO1[0, 2000, 1], dhT1[0, 2] = float("inf"), -float("inf"), float("inf")
+    _, _, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+    gr = ops.linrec_bwd(x, g, st, dO1, beta=b, dh_T=dhT1)
+    for c, t, v in ((0, 2490, float("inf")), (1, 2000, -float("inf")), (2, 2499, float("inf"))):
+        assert bool((gr["dx"][0, :t + 1, c] == v).all()) and gr["dh0"][0, c] == v
+    ref = R.grads_and_bounds(x, g, b, s, dO, dhT)
+    for n in ("dx", "dg", "dbeta"):
+        R.check(n, gr[n][:, :, 3:], *(t[:, :, 3:] for t in ref[n]))
+
+
+def test_a_step_forgets_what_is_not_finite():
+    announce("linrec_step_border")
+    x, g, b, _, _, _ = R.inputs(3, 1, 10, torch.float32, True, False, seed=71)
+    x, g, b = x[:, 0], g[:, 0], b[:, 0]
+    g[:, :5] = -float("inf")
+    for bad in BAD:
+        h = torch.full((3, 10), bad, device="cuda")
+        o = ops.linrec_step(x, g, h, beta=b)
+        assert torch.equal(o[:, :5], (x * b)[:, :5]) and torch.equal(h[:, :5], o[:, :5])
+        assert not bool(torch.isfinite(o[:, 5:]).any()) and not bool(torch.isfinite(h[:, 5:]).any())
+
+
 class Margins:
     """A tensor inside a buffer of NaN patterns, 64 KiB of them on each side."""
 
