@@ -492,17 +492,27 @@ def _enqueue(gpu: int, fn, *args):
 def _on_stream(stream, name: str, t: torch.Tensor, fn, *args):
     """``fn(*args)`` with ``stream`` current.  What the call allocates belongs to that
     stream, so the kernels never write into memory that work queued elsewhere still
-    uses; the results are marked as used on the caller's stream too."""
+    uses; the results are marked as used on the caller's stream too, and the tensors
+    given as used on ``stream``, so that the caller may let go of either at once."""
     gpu = _gpu(name, t)
     if stream.device.index != gpu:
         raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
     caller = torch.cuda.current_stream(gpu)
     with torch.cuda.stream(stream):
         res = fn(*args)
-    for r in res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else (res,):
-        if r is not None:
-            r.record_stream(caller)
+    if stream != caller:
+        _used_on(caller, res)
+        _used_on(stream, args)
     return res
+
+
+def _used_on(stream, given):
+    """Marks the tensors in ``given`` (a tensor, or a tuple or dict that may hold some)."""
+    if isinstance(given, torch.Tensor):
+        given.record_stream(stream)
+    elif isinstance(given, (tuple, dict)):
+        for v in given.values() if isinstance(given, dict) else given:
+            _used_on(stream, v)
 
 
 def _addr(t: Optional[torch.Tensor]):

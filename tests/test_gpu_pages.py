@@ -336,6 +336,62 @@ def test_token_steps_captured_and_replayed():
             assert torch.equal(a, b), i
 
 
+def test_inputs_may_go_after_a_call_on_another_stream():
+    """Temporaries given to calls on a busy stream, let go and their memory taken for other
+    values at once: the calls still see what they were given."""
+    import linrecref as R
+    announce("stream_inputs")
+    B, D, T, H, N = 4, 130, 300, 2, 9
+    x, g, b, s, dO, dhT = R.inputs(B, T, D, torch.float32, True, True, 0.1, seed=80)
+    _, _, st = ops.linrec_fwd(x, g, beta=b, h0=s, want_states=True)
+    rx, rg, rb = (v[:, 0].contiguous() for v in (x, g, b))
+    t = _step_inputs("gdn", "bf16", B, H, 64, 128, seed=81)
+    pool, other = (0.02 * torch.randn(N, H, 128, 64, device="cuda") for _ in range(2))
+    h = torch.randn(N, D, device="cuda")
+    slots, dst, src, live = _ints([3, 0, 8, 3]), _ints([1, 2]), _ints([3, -1]), _ints([8, -1, 0])
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def calls(take, stream):
+        """Every call that takes a stream, its inputs by way of ``take``."""
+        p, q = pool.clone(), h.clone()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        res = list(ops.linrec_fwd(take(x), take(g), beta=take(b), h0=take(s), want_states=True, workspace=take(ws), stream=stream))
+        res += ops.linrec_bwd(take(x), take(g), take(st), take(dO), beta=take(b), dh_T=take(dhT), stream=stream).values()
+        res.append(ops.linrec_step(take(rx), take(rg), q, beta=take(rb), slots=take(slots), stream=stream))
+        res.append(ops.delta_decode_slots("gdn", take(t["q"]), take(t["k"]), take(t["v"]), take(t["beta"]), p, take(slots),
+                                          g=take(t["g"]), stream=stream))
+        ops.pages_copy(p, take(dst), take(src), src_pool=take(other), stream=stream)
+        res += ops.pages_compact(q, take(live), stream=stream)
+        return res + [p, q[:2]]
+
+    want = calls(lambda v: v, None)
+    side, taken = torch.cuda.Stream(), []
+    big = torch.ones(1 << 28, device="cuda")
+
+    def take(v):
+        c = v.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        taken.append(v)
+        return c
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(200):                                 # 80 ms and more
+            big.mul_(1.0)
+        busy = torch.cuda.Event()
+        busy.record()
+    got = calls(take, side)
+    junk = [torch.full_like(v, 7) for v in 3 * taken]
+    torch.cuda.current_stream().synchronize()
+    late = not busy.query()                                  # nothing above had begun when its inputs went
+    side.synchronize()
+    del junk
+    assert late
+    for i, (a, c) in enumerate(zip(got, want)):
+        assert torch.equal(a, c), i
+
+
 def test_refusals():
     pool = torch.zeros(4, 8, device="cuda")
     i = _ints([0, 1])
