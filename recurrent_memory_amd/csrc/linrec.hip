@@ -452,37 +452,38 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_fwd_kernel(LinrecArg
         forget_derived(xr);
         if constexpr (BETA) forget_derived(br);
         wave_start<VEC>(J, ts, w, w, waves, q, p.h0, at.ch, channels, at.nch, h);
-        if (at.nch == 0 || n == 0) continue;
-        if (p.states != nullptr) {
-            float* s = p.states + (at.seq * blocks + t0 / kTok) * p.D + at.c;
+        if (at.nch > 0 && n > 0) {             // all lanes go on to the next tile's barrier
+            if (p.states != nullptr) {
+                float* s = p.states + (at.seq * blocks + t0 / kTok) * p.D + at.c;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (v < at.nch) s[v] = h[v];
-        }
-        typename W::T* o = static_cast<typename W::T*>(p.o) + row;
-        auto finish = [&](auto forgets) {
-            float a[VEC], u[VEC];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                token(i, a, u);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
-                if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+                for (int v = 0; v < VEC; ++v)
+                    if (v < at.nch) s[v] = h[v];
             }
-        };
-        if (__builtin_expect(forgets, 0)) {
-            forget_derived(gr);
-            forget_derived(xr);
-            if constexpr (BETA) forget_derived(br);
-            finish(std::true_type());
-        } else {
-            finish(std::false_type());
-        }
-        // beyond the last token h is carried along unchanged
-        if (p.hT != nullptr && t0 + n == p.T) {
+            typename W::T* o = static_cast<typename W::T*>(p.o) + row;
+            auto finish = [&](auto forgets) {
+                float a[VEC], u[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (v < at.nch) p.hT[at.ch + v] = h[v];
+                for (int i = 0; i < kTok; ++i) {
+                    token(i, a, u);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                    if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+                }
+            };
+            if (__builtin_expect(forgets, 0)) {
+                forget_derived(gr);
+                forget_derived(xr);
+                if constexpr (BETA) forget_derived(br);
+                finish(std::true_type());
+            } else {
+                finish(std::false_type());
+            }
+            // beyond the last token h is carried along unchanged
+            if (p.hT != nullptr && t0 + n == p.T) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    if (v < at.nch) p.hT[at.ch + v] = h[v];
+            }
         }
     }
 }
@@ -548,87 +549,88 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwd
         forget_derived(gr);
         forget_derived(dr);
         wave_start<VEC>(J, ts, w, pos, waves, q, p.dhT, at.ch, channels, at.nch, r);
-        if (!here) continue;
-        // The states before each token, from the one that the forward pass kept: those of
-        // every fourth token first, then, from the last four tokens to the first, the
-        // ones between (all sixteen at once do not fit beside the inputs in 128 registers).
-        typedef typename W::T T;
-        auto finish = [&](auto forgets) {
-            auto advance = [&](int i) {
-                float a[VEC], u[VEC], b[VEC];
-                decay(i, a);
-                W::unpack(xr[i], u);
-                if constexpr (BETA) W::unpack(br[i], b);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    if constexpr (BETA) u[v] *= b[v];
-                    h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
-                }
-            };
-            constexpr int kPart = 4;
-            float start[kTok / kPart][VEC];
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                if (i % kPart == 0) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
-                }
-                if (i < kTok - kPart) advance(i);
-            }
-#pragma unroll
-            for (int part = kTok / kPart - 1; part >= 0; --part) {
-                float before[kPart][VEC];
-                forget_derived(gr);
-                forget_derived(xr);
-                if constexpr (BETA) forget_derived(br);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
-#pragma unroll
-                for (int i = 0; i < kPart; ++i) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
-                    if (i + 1 < kPart) advance(part * kPart + i);
-                }
-#pragma unroll
-                for (int j = kPart - 1; j >= 0; --j) {
-                    const int i = part * kPart + j;
-                    float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
+        if (here) {                            // all lanes go on to the next tile's barrier
+            // The states before each token, from the one that the forward pass kept: those of
+            // every fourth token first, then, from the last four tokens to the first, the
+            // ones between (all sixteen at once do not fit beside the inputs in 128 registers).
+            typedef typename W::T T;
+            auto finish = [&](auto forgets) {
+                auto advance = [&](int i) {
+                    float a[VEC], u[VEC], b[VEC];
                     decay(i, a);
-                    W::unpack(dr[i], e);
-                    W::unpack(xr[i], x);
+                    W::unpack(xr[i], u);
                     if constexpr (BETA) W::unpack(br[i], b);
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) {
-                        e[v] += r[v];
-                        r[v] = forgets ? apply(a[v], e[v], 0.f) : a[v] * e[v];
-                        dg[v] = forgets ? apply(a[v], before[j][v] * e[v], 0.f) : r[v] * before[j][v];
-                        if constexpr (BETA) {
-                            x[v] *= e[v];
-                            e[v] *= b[v];
+                        if constexpr (BETA) u[v] *= b[v];
+                        h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                    }
+                };
+                constexpr int kPart = 4;
+                float start[kTok / kPart][VEC];
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    if (i % kPart == 0) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
+                    }
+                    if (i < kTok - kPart) advance(i);
+                }
+#pragma unroll
+                for (int part = kTok / kPart - 1; part >= 0; --part) {
+                    float before[kPart][VEC];
+                    forget_derived(gr);
+                    forget_derived(xr);
+                    if constexpr (BETA) forget_derived(br);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
+#pragma unroll
+                    for (int i = 0; i < kPart; ++i) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
+                        if (i + 1 < kPart) advance(part * kPart + i);
+                    }
+#pragma unroll
+                    for (int j = kPart - 1; j >= 0; --j) {
+                        const int i = part * kPart + j;
+                        float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
+                        decay(i, a);
+                        W::unpack(dr[i], e);
+                        W::unpack(xr[i], x);
+                        if constexpr (BETA) W::unpack(br[i], b);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            e[v] += r[v];
+                            r[v] = forgets ? apply(a[v], e[v], 0.f) : a[v] * e[v];
+                            dg[v] = forgets ? apply(a[v], before[j][v] * e[v], 0.f) : r[v] * before[j][v];
+                            if constexpr (BETA) {
+                                x[v] *= e[v];
+                                e[v] *= b[v];
+                            }
+                        }
+                        if (i < n) {
+                            const int64_t el = row + static_cast<int64_t>(i) * p.D;
+                            W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
+                            W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
+                            if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
                         }
                     }
-                    if (i < n) {
-                        const int64_t el = row + static_cast<int64_t>(i) * p.D;
-                        W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
-                        W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
-                        if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
-                    }
                 }
+            };
+            if (__builtin_expect(forgets, 0)) {
+                forget_derived(gr);
+                forget_derived(xr);
+                forget_derived(dr);
+                if constexpr (BETA) forget_derived(br);
+                finish(std::true_type());
+            } else {
+                finish(std::false_type());
             }
-        };
-        if (__builtin_expect(forgets, 0)) {
-            forget_derived(gr);
-            forget_derived(xr);
-            forget_derived(dr);
-            if constexpr (BETA) forget_derived(br);
-            finish(std::true_type());
-        } else {
-            finish(std::false_type());
-        }
-        if (p.dh0 != nullptr && t0 == 0) {
+            if (p.dh0 != nullptr && t0 == 0) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (v < at.nch) p.dh0[at.ch + v] = r[v];
+                for (int v = 0; v < VEC; ++v)
+                    if (v < at.nch) p.dh0[at.ch + v] = r[v];
+            }
         }
     }
 }

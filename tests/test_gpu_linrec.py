@@ -436,6 +436,24 @@ def test_more_tiles_than_workgroups(B, T, D):
     assert torch.equal(gr["dg"], (e * torch.cat((torch.zeros_like(h[:, :1]), h[:, :-1]), 1)).float())
 
 
+def test_workgroups_go_on_after_a_partly_filled_column():
+    """40000 columns of three tiles, the last column of 61 lanes: the workgroup that has it in
+    its first turn takes another tile after it, and the last tiles have waves without tokens."""
+    B, T, D = 1, 257, 40000 * 64 - 3
+    announce("linrec_partial_column", B, T, D)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    x = torch.randint(-2, 3, (B, T, D), generator=gen, device="cuda").float()
+    g = torch.zeros_like(x)
+    o, hT, st = ops.linrec_fwd(x, g, want_states=True)
+    h = torch.cumsum(x, 1)                                   # whole numbers below 2^24: exact
+    assert torch.equal(o, h) and torch.equal(hT, h[:, -1])
+    assert torch.equal(st[:, 1:], h[:, 15:-1:16]) and not bool(st[:, 0].any())
+    gr = ops.linrec_bwd(x, g, st, x)
+    e = torch.cumsum(x.flip(1), 1).flip(1)
+    assert torch.equal(gr["dx"], e) and torch.equal(gr["dh0"], e[:, 0])
+
+
 def test_second_derivatives_are_refused():
     x, g, b, s, dO, dhT = R.inputs(1, 20, 4, torch.float32, seed=22)
     x.requires_grad_(True)
