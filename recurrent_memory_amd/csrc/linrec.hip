@@ -22,10 +22,13 @@
 // is: 0 times an infinity would be NaN.  So does the map of a run that holds such a token;
 // a product of decays that only gets small stops at the smallest normal number instead
 // (which moves a state by at most 2^-126 of one before it), so that an infinity stays one.
-// A wave takes its 16 tokens without regard to this, and only if their product of decays
-// leaves the normal numbers in some lane again, with a selection for each token
-// (selections in every wave: backward 181 instead of 170 us at B=1 T=32768 D=2048 bf16; the
-// registers that the second form spills are spilled in that form only).
+// A wave takes its 16 tokens without regard to this.  If their product of decays leaves
+// the normal numbers in some lane, it reduces them once more with a selection for each; and
+// if then a decay was zero and a state or gradient ends not finite (none becomes finite
+// again on the way), it takes its outputs again, token by token, in a loop that needs few
+// registers (selections in every wave: backward 181 instead of 170 us at B=1 T=32768 D=2048
+// bf16; a second form of the unrolled code for the waves with a zero, which spills: 124
+// instead of 98 us at B=4 T=4096 D=2048 with a document's border every 512 tokens).
 //
 // Waiting.  A published word carries its own readiness: the workspace is filled with
 // all-ones (a NaN pattern that is never published) before the launch, and readers poll
@@ -214,6 +217,7 @@ struct Joint {
     float2 wave[kSingleWaves][64 * VEC];  // the waves' maps, in the order they act
     float2 tile[kMaxWaves - 1][64 * VEC]; // maps of the tiles before this one, of its group
     float carry[64 * VEC];                // the state in front of those
+    float start[kSingleWaves][64 * VEC];  // what wave_start() gave the waves that may begin again
     uint32_t ticket;
 };
 
@@ -382,7 +386,16 @@ __device__ __forceinline__ void forget_derived(uint32_t* r) {
     for (int i = 0; i < kTok; ++i) asm volatile("" : "+v"(r[i]));
 }
 
-// Whether a token of the wave may forget, from the products of its lanes' decays.
+// The word of one token, of a lane that has channels.
+template <typename W, bool UNI>
+__device__ __forceinline__ uint32_t load_token(const void* base, int64_t row, const Place<W, UNI>& at) {
+    const typename W::T* q = static_cast<const typename W::T*>(base) + row + at.c;
+    if (W::kOdd && at.lone) return static_cast<uint32_t>(*q);
+    return W::template load<false>(q);
+}
+
+// Whether a token of the wave may forget, from the products of its lanes' decays; after
+// join() made these, whether one does.
 template <int VEC>
 __device__ __forceinline__ bool any_forgets(const float* A) {
     bool normal = true;
@@ -390,11 +403,19 @@ __device__ __forceinline__ bool any_forgets(const float* A) {
     for (int v = 0; v < VEC; ++v) normal = normal && A[v] >= kSmallest;
     return __any(!normal);
 }
+template <int VEC>
+__device__ __forceinline__ bool all_finite(const float* f) {
+    bool finite = true;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) finite = finite && __builtin_isfinite(f[v]);
+    return finite;
+}
 
-// Six waves a SIMD, three workgroups of eight waves a CU, for a word of one channel and
-// without a gate, where at most the second form (see Forgetting) spills for it: B=4 T=4096
-// D=2048 bf16 without a gate 45.5 us, with five waves 47.8; D=1024 fp32 with one 53.9 us,
-// with four 55.3.  Two channels and a gate take 111 registers, two workgroups.
+// Six waves a SIMD, three workgroups of eight waves a CU, for words of one channel and
+// without a gate, which the compiler misses by a few registers (B=4 T=4096 D=2048 bf16
+// without a gate 44.7 us, with five waves 47.2; D=1024 fp32 with one 53.7 us, with five
+// 55.0; two registers spilled where rows are not whole waves).  Two channels and a gate take
+// a hundred registers, two workgroups.
 template <typename W, bool BETA, bool UNI, bool NT>
 __global__ __launch_bounds__(kSingleWaves * 64, BETA && W::VEC == 2 ? 1 : 6) void linrec_fwd_kernel(LinrecArgs p, Tiles ts) {
     constexpr int VEC = W::VEC;
@@ -443,12 +464,13 @@ __global__ __launch_bounds__(kSingleWaves * 64, BETA && W::VEC == 2 ? 1 : 6) voi
             }
         };
         reduce(std::false_type());
-        const bool forgets = any_forgets<VEC>(A);
+        bool forgets = any_forgets<VEC>(A);
         if (__builtin_expect(forgets, 0)) {
             forget_derived(gr);
             forget_derived(xr);
             if constexpr (BETA) forget_derived(br);
             reduce(std::true_type());
+            forgets = any_forgets<VEC>(A);
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) J.wave[w][lane * VEC + v] = make_float2(A[v], h[v]);
@@ -464,23 +486,35 @@ __global__ __launch_bounds__(kSingleWaves * 64, BETA && W::VEC == 2 ? 1 : 6) voi
                     if (v < at.nch) s[v] = h[v];
             }
             typename W::T* o = static_cast<typename W::T*>(p.o) + row;
-            auto finish = [&](auto forgets) {
-                float a[VEC], u[VEC];
+            if (forgets) {
 #pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    token(i, a, u);
+                for (int v = 0; v < VEC; ++v) J.start[w][lane * VEC + v] = h[v];
+            }
+            float a[VEC], u[VEC];
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
-                    if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+            for (int i = 0; i < kTok; ++i) {
+                token(i, a, u);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[v], h[v], u[v]);
+                if (i < n) W::template store<NT>(o + static_cast<int64_t>(i) * p.D + at.c, h, at.lone);
+            }
+            if (__builtin_expect(forgets && !all_finite<VEC>(h), 0)) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = J.start[w][lane * VEC + v];
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const int64_t el = row + static_cast<int64_t>(i) * p.D;
+                    float b[VEC];
+                    W::unpack(load_token<W>(p.x, el, at), u);
+                    W::unpack(load_token<W>(p.g, el, at), a);
+                    if constexpr (BETA) W::unpack(load_token<W>(p.beta, el, at), b);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        if constexpr (BETA) u[v] *= b[v];
+                        h[v] = apply(__expf(a[v]), h[v], u[v]);
+                    }
+                    W::template store<NT>(static_cast<typename W::T*>(p.o) + el + at.c, h, at.lone);
                 }
-            };
-            if (__builtin_expect(forgets, 0)) {
-                forget_derived(gr);
-                forget_derived(xr);
-                if constexpr (BETA) forget_derived(br);
-                finish(std::true_type());
-            } else {
-                finish(std::false_type());
             }
             // beyond the last token h is carried along unchanged
             if (p.hT != nullptr && t0 + n == p.T) {
@@ -542,11 +576,12 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwd
             }
         };
         reduce(std::false_type());
-        const bool forgets = any_forgets<VEC>(A);
+        bool forgets = any_forgets<VEC>(A);
         if (__builtin_expect(forgets, 0)) {
             forget_derived(gr);
             forget_derived(dr);
             reduce(std::true_type());
+            forgets = any_forgets<VEC>(A);
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) J.wave[pos][lane * VEC + v] = make_float2(A[v], r[v]);
@@ -558,77 +593,113 @@ __global__ __launch_bounds__(kSingleWaves * 64) void linrec_bwd_kernel(LinrecBwd
             // every fourth token first, then, from the last four tokens to the first, the
             // ones between (all sixteen at once do not fit beside the inputs in 128 registers).
             typedef typename W::T T;
-            auto finish = [&](auto forgets) {
-                auto advance = [&](int i) {
-                    float a[VEC], u[VEC], b[VEC];
+            auto advance = [&](int i) {
+                float a[VEC], u[VEC], b[VEC];
+                decay(i, a);
+                W::unpack(xr[i], u);
+                if constexpr (BETA) W::unpack(br[i], b);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    if constexpr (BETA) u[v] *= b[v];
+                    h[v] = fmaf(a[v], h[v], u[v]);
+                }
+            };
+            if (forgets) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) J.start[w][lane * VEC + v] = r[v];
+            }
+            constexpr int kPart = 4;
+            float start[kTok / kPart][VEC];
+            bool finite = true;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                if (i % kPart == 0) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
+                }
+                if (i < kTok - kPart) advance(i);
+            }
+#pragma unroll
+            for (int part = kTok / kPart - 1; part >= 0; --part) {
+                float before[kPart][VEC];
+                forget_derived(gr);
+                forget_derived(xr);
+                if constexpr (BETA) forget_derived(br);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
+                    if (i + 1 < kPart) advance(part * kPart + i);
+                }
+                if (part == kTok / kPart - 1) finite = all_finite<VEC>(before[kPart - 1]);
+#pragma unroll
+                for (int j = kPart - 1; j >= 0; --j) {
+                    const int i = part * kPart + j;
+                    float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
                     decay(i, a);
-                    W::unpack(xr[i], u);
+                    W::unpack(dr[i], e);
+                    W::unpack(xr[i], x);
                     if constexpr (BETA) W::unpack(br[i], b);
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) {
-                        if constexpr (BETA) u[v] *= b[v];
-                        h[v] = forgets ? apply(a[v], h[v], u[v]) : fmaf(a[v], h[v], u[v]);
+                        e[v] += r[v];
+                        r[v] = a[v] * e[v];
+                        dg[v] = r[v] * before[j][v];
+                        if constexpr (BETA) {
+                            x[v] *= e[v];
+                            e[v] *= b[v];
+                        }
                     }
-                };
-                constexpr int kPart = 4;
-                float start[kTok / kPart][VEC];
-#pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    if (i % kPart == 0) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) start[i / kPart][v] = h[v];
+                    if (i < n) {
+                        const int64_t el = row + static_cast<int64_t>(i) * p.D;
+                        W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
+                        W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
+                        if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
                     }
-                    if (i < kTok - kPart) advance(i);
                 }
+            }
+            if (__builtin_expect(forgets && !(finite && all_finite<VEC>(r)), 0)) {
 #pragma unroll
-                for (int part = kTok / kPart - 1; part >= 0; --part) {
-                    float before[kPart][VEC];
-                    forget_derived(gr);
-                    forget_derived(xr);
-                    if constexpr (BETA) forget_derived(br);
+                for (int v = 0; v < VEC; ++v) r[v] = J.start[w][lane * VEC + v];
+#pragma unroll 1
+                for (int i = n - 1; i >= 0; --i) {
+                    float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
+                    const float* s = p.states + (at.seq * blocks + t0 / kTok) * p.D + at.c;
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) h[v] = start[part][v];
+                    for (int v = 0; v < VEC; ++v) h[v] = v < at.nch ? s[v] : 0.f;
+#pragma unroll 1
+                    for (int k = 0;; ++k) {
+                        const int64_t el = row + static_cast<int64_t>(k) * p.D;
+                        W::unpack(load_token<W>(p.x, el, at), x);
+                        W::unpack(load_token<W>(p.g, el, at), a);
+                        if constexpr (BETA) W::unpack(load_token<W>(p.beta, el, at), b);
 #pragma unroll
-                    for (int i = 0; i < kPart; ++i) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) before[i][v] = h[v];
-                        if (i + 1 < kPart) advance(part * kPart + i);
-                    }
-#pragma unroll
-                    for (int j = kPart - 1; j >= 0; --j) {
-                        const int i = part * kPart + j;
-                        float a[VEC], e[VEC], x[VEC], b[VEC], dg[VEC];
-                        decay(i, a);
-                        W::unpack(dr[i], e);
-                        W::unpack(xr[i], x);
-                        if constexpr (BETA) W::unpack(br[i], b);
+                        for (int v = 0; v < VEC; ++v) a[v] = __expf(a[v]);
+                        if (k == i) break;
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) {
-                            e[v] += r[v];
-                            r[v] = forgets ? apply(a[v], e[v], 0.f) : a[v] * e[v];
-                            dg[v] = forgets ? apply(a[v], before[j][v] * e[v], 0.f) : r[v] * before[j][v];
-                            if constexpr (BETA) {
-                                x[v] *= e[v];
-                                e[v] *= b[v];
-                            }
-                        }
-                        if (i < n) {
-                            const int64_t el = row + static_cast<int64_t>(i) * p.D;
-                            W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
-                            W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
-                            if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
+                            if constexpr (BETA) x[v] *= b[v];
+                            h[v] = apply(a[v], h[v], x[v]);
                         }
                     }
+                    const int64_t el = row + static_cast<int64_t>(i) * p.D;
+                    W::unpack(load_token<W>(p.dO, el, at), e);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        e[v] += r[v];
+                        r[v] = apply(a[v], e[v], 0.f);
+                        dg[v] = a[v] == 0.f ? 0.f : r[v] * h[v];
+                        if constexpr (BETA) {
+                            x[v] *= e[v];
+                            e[v] *= b[v];
+                        }
+                    }
+                    W::template store<NT>(static_cast<T*>(p.dx) + el + at.c, e, at.lone);
+                    W::template store<NT>(static_cast<T*>(p.dg) + el + at.c, dg, at.lone);
+                    if constexpr (BETA) W::template store<NT>(static_cast<T*>(p.dbeta) + el + at.c, x, at.lone);
                 }
-            };
-            if (__builtin_expect(forgets, 0)) {
-                forget_derived(gr);
-                forget_derived(xr);
-                forget_derived(dr);
-                if constexpr (BETA) forget_derived(br);
-                finish(std::true_type());
-            } else {
-                finish(std::false_type());
             }
             if (p.dh0 != nullptr && t0 == 0) {
 #pragma unroll

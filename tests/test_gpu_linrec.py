@@ -113,11 +113,12 @@ BAD = [float("inf"), -float("inf"), float("nan")]
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("border,at", [(1, 0), (20, 3), (20, 19), (33, 16), (130, 127), (256, 0), (700, 690), (2200, 5)])
-def test_a_border_stops_what_is_not_finite(dtype, border, at):
+@pytest.mark.parametrize("D", [66, 65])
+def test_a_border_stops_what_is_not_finite(D, dtype, border, at):
     """Nothing passes a token that forgets: an infinity or NaN written or handed in before
     it, or arriving as a gradient after it, changes no bit on its other side."""
-    announce("linrec_border", dtype, border, at)
-    B, T, D = 1, border + 300, 66
+    announce("linrec_border", D, dtype, border, at)
+    B, T = 1, border + 300
     x, g, b, s, dO, dhT = R.inputs(B, T, D, DT[dtype], True, True, 0.1, seed=border)
     g[:, border, ::2] = -float("inf")
     g[:, border, 1::2] = -88.0                               # zero in fp32 too
@@ -172,6 +173,38 @@ def test_an_infinity_outlives_small_decays(dtype, g0):
     ref = R.grads_and_bounds(x, g, b, s, dO, dhT)
     for n in ("dx", "dg", "dbeta"):
         R.check(n, gr[n][:, :, 3:], *(t[:, :, 3:] for t in ref[n]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("with_beta", [True, False])
+@pytest.mark.parametrize("D", [64, 71])
+def test_sequences_of_documents(D, with_beta, dtype):
+    """Borders in every 16 tokens and more seldom, an infinity or NaN in every third document:
+    each document is what it is by itself, and the finite ones have finite gradients."""
+    announce("linrec_documents", D, with_beta, dtype)
+    ends = [0, 3, 4, 11, 16, 30, 33, 64, 200, 201, 330, 700, 900]
+    T = ends[-1]
+    x, g, b, _, dO, _ = R.inputs(1, T, D, DT[dtype], with_beta, False, 0.2, seed=D)
+    for n, lo in enumerate(ends[:-1]):
+        g[:, lo] = -float("inf")
+        if n % 3 == 1:
+            x[:, lo + (ends[n + 1] - lo) // 2] = BAD[n // 3 % 3]
+            dO[:, ends[n + 1] - 1] = BAD[n // 3 % 3]
+    o, _, st = ops.linrec_fwd(x, g, beta=b, want_states=True)
+    gr = ops.linrec_bwd(x, g, st, dO, beta=b)
+    for n, (lo, hi) in enumerate(zip(ends, ends[1:])):
+        part = [None if v is None else v[:, lo:hi].contiguous() for v in (x, g, b)]
+        mid, got = (hi - lo) // 2, o[:, lo:hi]
+        if n % 3 == 1:
+            assert bool(torch.isfinite(got[:, :mid]).all()) and not bool(torch.isfinite(got[:, mid:]).any()), n
+            assert not bool(torch.isfinite(gr["dx"][:, lo:hi]).any()) and not bool(gr["dg"][:, lo].any()), n
+            continue
+        h, err = R.states_and_bounds(*part, None)
+        R.check("o", got, h[:, 1:], err[:, 1:])
+        for name, (v, e) in R.grads_and_bounds(*part, None, dO[:, lo:hi], None).items():
+            if name != "dh0":
+                R.check(name, gr[name][:, lo:hi], v, e)
+    assert not bool(gr["dh0"].any())
 
 
 def test_a_step_forgets_what_is_not_finite():
