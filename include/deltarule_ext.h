@@ -113,7 +113,9 @@ dr_status delta_linrec_bwd(const dr_linrec_desc* desc, const void* x, const void
  *          outside the pool (-1, say, for the rows that pad a batch) is skipped:
  *          its row of o is left as it was.  Rows that name the same page are
  *          applied one after the other, in the order of b.  NULL: row b's state
- *          is page b, and n_pages must be B
+ *          is page b, and n_pages must be B.  Every row looks through the list for
+ *          others of its page: meant for batches of up to some thousand rows (4096
+ *          rows of 256 channels 25 us, 65536 rows 3.9 ms)
  *   o      [B, D] dtype (written)
  *   Neither o nor h may overlap any input or each other.
  */
@@ -127,7 +129,8 @@ dr_status delta_linrec_step(const dr_linrec_desc* desc, const void* x, const voi
  *   desc and q, k, v, beta, wgate, g, o  as for delta_decode (T = 1)
  *   pool   [n_pages, H, d_v, d_k] fp32, updated in place
  *   slots  [B] int32, as for delta_linrec_step (required): rows outside the pool
- *          are skipped, rows that share a page act in the order of b
+ *          are skipped, rows that share a page act in the order of b; up to some
+ *          thousand rows
  *   Neither o nor pool may overlap any input or each other.
  */
 dr_status delta_decode_slots(const dr_desc* desc, const void* q, const void* k, const void* v,
@@ -153,7 +156,10 @@ typedef struct {
  *
  * The entries act as if one after the other, in order: a page may be named any
  * number of times on either side.  Lists in which no destination is named twice
- * or is also a source (every list of forks into free pages) run fastest.
+ * or is also a source (every list of forks into free pages) are copied at once;
+ * one such entry makes the call apply its whole list in order, at 0.3 to 1 us an
+ * entry (4000 pages of 8 KiB: 18 us at once, 1.95 ms in order).  A move, a copy
+ * and then the clear of its source, is quicker as two calls.
  */
 dr_status delta_pages_copy(const dr_pages_desc* desc, float* pool, const int32_t* dst,
                            const float* src_pool, int32_t src_pages, const int32_t* src,

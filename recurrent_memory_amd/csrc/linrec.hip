@@ -28,7 +28,7 @@
 // again on the way), it takes its outputs again, token by token, in a loop that needs few
 // registers (selections in every wave: backward 181 instead of 170 us at B=1 T=32768 D=2048
 // bf16; a second form of the unrolled code for the waves with a zero, which spills: 124
-// instead of 98 us at B=4 T=4096 D=2048 with a document's border every 512 tokens).
+// instead of 100 us at B=4 T=4096 D=2048 with a document's border every 512 tokens).
 //
 // Waiting.  A published word carries its own readiness: the workspace is filled with
 // all-ones (a NaN pattern that is never published) before the launch, and readers poll
@@ -63,11 +63,11 @@ __device__ __forceinline__ float apply(float a, float h, float c) { return a == 
 __device__ __forceinline__ float join(float A, float a) { return A == 0.f || a == 0.f ? 0.f : fmaxf(A * a, kSmallest); }
 
 // Memory accesses of the tiles.  NT: non-temporal, where rows are whole cache lines and
-// every line passes once (B=1 T=32768 D=2048 bf16: forward 109 us plain, 102 us
-// non-temporal, backward 185 and 170 us; D=2112, where a wave's end falls inside a row,
-// B=4 T=4096: forward 66 and 60 us, backward 110 and 101 us); plain where two waves share
-// lines, which then meet in a cache (B=3 T=8000 D=1000 bf16: forward 55 us plain, 59 us
-// non-temporal; backward 99 and 118 us).
+// every line passes once (B=1 T=32768 D=2048 bf16: forward 112 us plain, 106 us
+// non-temporal, backward 185 and 169 us; D=2112, where a wave's end falls inside a row,
+// B=4 T=4096: forward 67 and 61 us, backward 113 and 102 us); plain where two waves share
+// lines, which then may meet in a cache (B=3 T=8000 D=1000 bf16: forward 56 us plain, 60 us
+// non-temporal; backward 100 and 118 us; T=4000 D=1001 fp32: 54 and 62, 104 and 129 us).
 template <bool NT, typename P>
 __device__ __forceinline__ P load_word(const P* p) {
     if constexpr (NT) return __builtin_nontemporal_load(p);
@@ -313,7 +313,7 @@ __device__ __forceinline__ bool next_tile(Joint<VEC>& J, const Tiles& ts, uint32
     // A different column first in each turn of the columns: workgroups go round the eight
     // XCDs, and with the same columns always on the same XCD, its L2 would see a few
     // residues of the row's addresses only, a few of its channels (B=1 T=32768 D=2048
-    // bf16 forward: 121 us so, 102 us with the columns turned).
+    // bf16 forward: 125 us so, 106 us with the columns turned).
     *column = (k % ts.columns + k / ts.columns) % ts.columns;
     *q = 0;
     if (turn > 0) __syncthreads();      // the last tile's LDS is no longer read
@@ -779,7 +779,7 @@ __global__ __launch_bounds__(kStepThreads) void linrec_step_kernel(LinrecStepArg
 // ---- plans ----
 
 // Tiles of a sequence.  One tile needs no counter, no maps and no clearing of them
-// (B=32 T=200 D=2048 bf16: forward 25 us as two tiles, 23 us as one; backward 43 and 37).
+// (B=32 T=200 D=2048 bf16: forward 26 us as two tiles, 23 us as one; backward 40 and 37).
 int64_t chain_of(int T) {
     if (T <= kSingleWaves * kTok) return 1;
     return (static_cast<int64_t>(T) + kMaxWaves * kTok - 1) / (kMaxWaves * kTok);

@@ -6,7 +6,10 @@
 // itself from a bitmap of the pool's pages in LDS (one bit a page, 8 KiB at most),
 // so that a call is one launch without workspace; a workgroup then takes 16 KiB
 // pieces of pages in turn, four 16-byte loads a lane in flight (32 KiB pieces and 2048
-// workgroups took 149 us for 250 MiB copied, this 104 us: 5.0 TB/s).
+// workgroups took 149 us for 250 MiB copied, this 104 us: 5.0 TB/s).  The plan is what
+// bounds long lists of small pages: each workgroup reads the whole list (a copy within one
+// pool twice) and marks its bitmap, 32768 copies of 64 floats 53 us for about 3 us of page
+// traffic, 65536 slots compacted 33 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -43,10 +46,13 @@ __device__ __forceinline__ void copy_piece(float* dst, const float* src, int64_t
 }
 
 // Pages of up to 128 vectors, `count` of them, as one run of vectors, so that every lane
-// has work (pages of 16 vectors: 32768 copies 95 us a workgroup a page, 55 us so; a page
-// of 512 vectors fills a workgroup, which then looks its numbers up once: 48 copies 4.4
-// us, 5.1 us so).  find(k, &dst, &src) gives the k-th copy's pages (src == nullptr
-// clears), or false if there is nothing to do.
+// has work.  Calls of 16384 copies, us, a workgroup a page and so:  16 vectors 48 and 27,
+// 64: 47 and 36, 128: 51 and 39, 256: 53 and 48, 512: 68 and 67; 32768 slots compacted, half of them
+// live:  16: 35 and 21, 64: 35 and 22, 128: 35 and 25, 256: 37 and 38, 384: 40 and 45,
+// 512: 41 and 54.  Short lists (48 entries) are the same up to 384 vectors; a page of 512 fills a
+// workgroup, which then looks its numbers up once: 48 copies 4.4 us, 5.1 us so.
+// find(k, &dst, &src) gives the k-th copy's pages (src == nullptr clears), or false if
+// there is nothing to do.
 constexpr int kSmallPage = kThreads / 2;
 template <int V, typename Find>
 __device__ __forceinline__ void copy_small_pages(int64_t count, uint32_t n, Find find) {
@@ -92,7 +98,10 @@ __device__ __forceinline__ bool acts(const PagesCopyArgs& p, int s, int d, bool 
 // source, the order does not matter and the pieces of all entries are copied at
 // once, by position (piece 0 of every entry, then piece 1, ...), so that the
 // forks of one page read it from cache.  Otherwise a lane owns a column of the
-// pages and applies the whole list to it in order: slower, and right for any list.
+// pages and applies the whole list to it in order, one load and store after another:
+// right for any list, and slow (4000 copies of 8 KiB pages 18 us, with one page named twice
+// 1.95 ms; of 256-byte pages 10 us and 1.26 ms; 200 pages of 1 MiB copied 85 us, moved as
+// copies each followed by a clear of its source 265 us).
 template <int V>
 __global__ __launch_bounds__(kThreads) void pages_copy_kernel(PagesCopyArgs p) {
     __shared__ uint32_t written[kWords];

@@ -7,8 +7,11 @@ namespace dr {
 
 // Row b's page, and whether a row before b, or one after it, names that page too.
 // Every wave scans the list by itself, 256 entries at a time, so that the answer is
-// wave-uniform without a barrier.  Called by whole waves.  The first 256 are loaded along with the row's own
-// entry, before either is looked at, so that a batch of up to 256 rows waits once.
+// wave-uniform without a barrier; that is quadratic in B, and made for batches of up to
+// some thousand rows (a step of 256 fp32 channels: 1024 rows 9 us with or without slots,
+// 4096 rows 25 us against 8, 16384 rows 272 against 15, 65536 rows 3.9 ms against 48 us).
+// Called by whole waves.  The first 256 are loaded along with the row's own entry, before
+// either is looked at, so that a batch of up to 256 rows waits once.
 __device__ __forceinline__ int slot_of_row(const int* __restrict__ slots, int B, int b, bool* earlier,
                                            bool* later) {
     const int lane = threadIdx.x & 63;
